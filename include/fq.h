@@ -57,7 +57,7 @@ typedef enum {
   FQ_ERR_TIMEOUT = 6      /* a bounded device-side wait gave up (see fq_wait_status) */
 } fq_status;
 
-typedef enum { FQ_F16 = 0, FQ_F32 = 1 } fq_dtype;
+typedef enum { FQ_F16 = 0, FQ_F32 = 1, FQ_BF16 = 2 } fq_dtype; /* FQ_BF16: fq_kv4_* only */
 
 /* Search-index kinds for fq_build_search_index. */
 typedef enum {
@@ -321,6 +321,110 @@ fq_status fq_selftest_wait_timeout(uint32_t polls, void* stream);
 fq_status fq_build_search_index(const float* codebook_host, int d, int k, int N, int kind,
                                 int L, int c, void* index_host, size_t index_capacity,
                                 size_t* index_bytes);
+
+/*
+ * The 4-bit paged cache (no counterpart in the paper; its "per-token INT" baseline with groups).
+ *
+ * Keys and values of a token are kept as 4-bit integers per coordinate with one step s and one
+ * zero z (fp16 each) per group of `group` consecutive coordinates: c in 0..15 stands for c s + z.
+ * The cache is a pool of n_blocks pages of `page` tokens that sequences reach through block
+ * tables, so a sequence grows without moving and pages go back to the pool when it ends.
+ *
+ * Limits: d = 64 or 128; group = 32, 64 or 128 dividing d; page a power of two, 16 .. 1024;
+ * n_blocks * page < 2^31.  Slot s of the pool is token s % page of page s / page.
+ *
+ * cache [n_blocks, Hkv, page / 16, fq_kv4_unit_bytes(d, group)] bytes, 16-byte aligned: units of 16
+ * consecutive tokens t = 0..15 of one kv head.  With NG = d / group, a unit holds in order
+ *   key codes    16 rows of d/2 bytes, token t in row r(t) = 2 (t & 3) + ((t >> 2) & 1) + (t & 8);
+ *                a row is d/8 32-bit words, coordinates 8w .. 8w + 7 (lowest in the lowest 4 bits)
+ *                in word (w & 3) (d/32) + (w >> 2);
+ *   value codes  16 rows of d/2 bytes, token t in row t; coordinates 8w .. 8w + 7 in word w, for
+ *                d = 128 in word w ^ 8 where t & 2;
+ *   key s, z     16 rows of 2 NG fp16, token t in row r(t): s of each group, then z of each group;
+ *   value s, z   16 rows of 2 NG fp16, token t in row t: (s, z) of each group.
+ */
+
+/* Bytes of one unit: 16 d + 128 d / group; 0 when (d, group) is unsupported. */
+size_t fq_kv4_unit_bytes(int d, int group);
+
+/*
+ * fq_page_step - advances block tables, free list and lengths by one serving step and gives every
+ * new token its slot.  All arrays are int32 on the device, 4-byte aligned.
+ *   lens, new_lens   [B]: tokens that a request holds (clamped to 0 .. max_blocks * page) and
+ *                    tokens that it adds now; new_lens < 0: the request ends and its pages go back.
+ *   block_tables     [B, max_blocks], updated in place: entries behind a request's pages are
+ *                    written as it grows, all others (a finished request's too) stay as they are.
+ *   free_list        [n_blocks], a stack updated in place: entries below *free_count are free pages.
+ *                    Pages of finished requests are pushed in request order, then the a-th new page
+ *                    of the step is the a-th from the top; entries above stay as they are.
+ *   free_count       [1] in; free_count_out [1] out.  lens_out [B] out: 0 for a finished request.
+ *                    free_count_out may be free_count and lens_out may be lens; no other arrays
+ *                    may overlap.
+ *   cu_new           [B + 1] out: exclusive sums of max(new_lens, 0), the requests' first new tokens
+ *                    (saturating at 2^31 - 1).
+ *   slots            [n_slots] out: the slot of each new token, request by request; -1 for the
+ *                    tokens of a refused request, for tokens on a page outside the pool and behind
+ *                    the last new token.
+ *   refused          [1] out: requests that were refused.  A request is refused, its length, table
+ *                    and pages left as they were, when it would pass max_blocks, when its tokens
+ *                    pass n_slots, or when it needs pages and the pages needed up to and including
+ *                    it are more than there are.
+ * Precondition: the table entries of held pages and the free list hold distinct pages of the pool.
+ * B <= 8192, max_blocks * page <= 2^30, n_slots <= 2^30.  One launch.
+ */
+fq_status fq_page_step(const int32_t* lens, const int32_t* new_lens, int B, int32_t* block_tables,
+                       int max_blocks, int page, int32_t* free_list, int n_blocks,
+                       const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
+                       int32_t* cu_new, int32_t* slots, int n_slots, int32_t* refused,
+                       void* stream);
+
+/*
+ * fq_kv4_write - quantises new keys and values and writes them at their slots.
+ *   k, v      n tokens of Hkv heads of d coordinates, fp16, bf16 or fp32 (type); token and head
+ *             strides in elements (for example slices of a fused projection's output), coordinates
+ *             contiguous.  16-byte aligned rows are read with wide loads.
+ *   slots     [n] int32: a token whose slot is outside [0, n_blocks * page) is not written.  A slot
+ *             given to two tokens of one call holds an unspecified mix of the two.
+ *   k_values, v_values  [n, Hkv, d] of `type`, 16-byte aligned, or NULL: what the codes stand for,
+ *             c s + z rounded to `type`, for every token (for a prefill that attends to its own
+ *             tokens as later steps will see them).
+ * In fp32, per group: z = fp16(min), s = fp16((max - z) * fp32(1/15)) (both within +-65504),
+ * c = clamp(rint((x - z) * (1 / s)), 0, 15), c = 0 where s = 0.
+ */
+fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, int Hkv, int d,
+                       int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                       int64_t v_head_stride, const int32_t* slots, uint8_t* cache,
+                       int64_t n_blocks, int page, int group, void* k_values, void* v_values,
+                       void* stream);
+
+/* Workspace bytes of fq_kv4_attn (a value of d alone), or 0 when d is unsupported. */
+size_t fq_kv4_attn_workspace_bytes(int d);
+
+/*
+ * fq_kv4_attn - causal attention of one or more query tokens per sequence over the 4-bit cache:
+ *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, g]) v[t, g],  g = h / (Hq / Hkv).
+ *   q         n_q tokens of Hq heads of d coordinates, fp16 or bf16 (type); token and head strides
+ *             in elements, coordinates contiguous.
+ *   cu_q      [B + 1] int32: sequence b's query tokens are rows cu_q[b] .. cu_q[b + 1) of q (at most
+ *             max_q of them).  NULL: one query token per sequence (n_q = B, max_q = 1).
+ *   kv_lens   [B] int32, clamped to 0 .. max_blocks * page: tokens of sequence b in the cache, its
+ *             query tokens (its last ones) included.  Query token i of m sees the tokens below
+ *             e = kv_len - m + i + 1 and, with window > 0, not below e - window.
+ *   block_tables  [B, max_blocks] int32: a sequence's pages in order.  Tokens on a page outside
+ *             [0, n_blocks) are not seen.  Nothing that is not seen is read into the result: it
+ *             may hold anything.
+ *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
+ *             sequence has are left as they were.
+ *   workspace fq_kv4_attn_workspace_bytes(d) bytes, 16-byte aligned, owned by the caller and
+ *             overwritten; calls that may overlap (two streams, two captured graphs) need one each.
+ * B <= 8192, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.
+ */
+fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
+                      int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_q, int B,
+                      int max_q, const uint8_t* cache, int64_t n_blocks, int Hkv, int page,
+                      int group, const int32_t* block_tables, int max_blocks,
+                      const int32_t* kv_lens, int window, float scale, void* out,
+                      void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,98 @@
+// The 4-bit paged key/value cache: layout of a unit and the launchers of its kernels.
+//
+// A unit holds 16 consecutive tokens of one kv head, keys and values, as fq.h describes it.  Its
+// parts and the order of their rows are those of the attention kernel's matrix fragments, so that
+// a warp reads each part with full-width shared-memory loads and no bank conflicts; a token's
+// codes and a token's steps and zeros are each contiguous, so that a write touches whole sectors.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstddef>
+#include <cstdint>
+
+#include "fq.h"
+
+namespace fq {
+namespace kv4 {
+
+constexpr int kUnit = 16;            // tokens of a unit
+constexpr int kMaxRequests = 8192;   // requests of one page step (their scans sit in shared memory)
+constexpr int kMinPage = 16, kMaxPage = 1024;
+
+__host__ __device__ constexpr int unit_bytes(int d, int group) {
+  return kUnit * d + 128 * (d / group);
+}
+// byte offsets of a unit's parts
+__host__ __device__ constexpr int off_v(int d) { return kUnit * d / 2; }
+__host__ __device__ constexpr int off_ks(int d) { return kUnit * d; }
+__host__ __device__ constexpr int off_vs(int d, int group) { return kUnit * d + 64 * (d / group); }
+
+// row of token t (0..15) in the key parts
+__host__ __device__ constexpr int key_row(int t) { return 2 * (t & 3) + ((t >> 2) & 1) + (t & 8); }
+// 32-bit word (8 coordinates) w of a key row sits at this word of the row ...
+__host__ __device__ constexpr int key_word(int w, int d) { return (w & 3) * (d / 32) + (w >> 2); }
+// ... and of token t's value row at this one
+__host__ __device__ constexpr int value_word(int w, int t, int d) {
+  return d == 128 ? w ^ (((t >> 1) & 1) << 3) : w;
+}
+
+struct WriteArgs {
+  const void* k;
+  const void* v;
+  fq_dtype type;
+  int64_t n;
+  int hkv, d;
+  int64_t k_tok, k_head, v_tok, v_head;  // strides in elements
+  const int32_t* slots;
+  uint8_t* cache;
+  int64_t n_blocks;
+  int page, group;
+  void* k_values;
+  void* v_values;
+};
+
+struct AttnArgs {
+  const void* q;
+  fq_dtype type;
+  int64_t n_q;
+  int hq, d;
+  int64_t q_tok, q_head;  // strides in elements
+  const int32_t* cu_q;
+  int B, max_q;
+  const uint8_t* cache;
+  int64_t n_blocks;
+  int hkv, page, group;
+  const int32_t* tables;
+  int max_blocks;
+  const int32_t* kv_lens;
+  int window;
+  float scale;
+  void* out;
+  void* workspace;
+};
+
+struct PageArgs {
+  const int32_t* lens;
+  const int32_t* new_lens;
+  int B;
+  int32_t* tables;
+  int max_blocks, page;
+  int32_t* free_list;
+  int n_blocks;
+  const int32_t* free_count;
+  int32_t* lens_out;
+  int32_t* free_count_out;
+  int32_t* cu_new;
+  int32_t* slots;
+  int n_slots;
+  int32_t* refused;
+};
+
+cudaError_t launch_write(const WriteArgs& a, cudaStream_t st);
+cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
+cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st);
+size_t attn_workspace_bytes(int d);
+
+}  // namespace kv4
+}  // namespace fq
