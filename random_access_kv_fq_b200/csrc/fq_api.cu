@@ -5,6 +5,7 @@
 
 #include "fq_internal.h"
 #include "codec_sm100.h"
+#include "kv4.h"
 
 namespace fq {
 
@@ -376,7 +377,8 @@ fq_status fq_wait_status(unsigned* timed_out, int clear) {
                                                wait_timeouts_encode_highk,
                                                wait_timeouts_encode_grid,
                                                wait_timeouts_decode, wait_timeouts_decode_large,
-                                               wait_timeouts_attn, wait_timeouts_selftest};
+                                               wait_timeouts_attn, wait_timeouts_selftest,
+                                               kv4::wait_timeouts_kv4};
   for (auto rd : readers)
     if (rd(clear != 0, &n) != cudaSuccess) return FQ_ERR_CUDA;
   if (timed_out) *timed_out = n;

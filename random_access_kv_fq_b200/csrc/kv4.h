@@ -93,6 +93,7 @@ cudaError_t launch_write(const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st);
 size_t attn_workspace_bytes(int d);
+cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_internal.h
 
 }  // namespace kv4
 }  // namespace fq

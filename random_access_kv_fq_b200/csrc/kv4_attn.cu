@@ -1,111 +1,803 @@
-// Attention over the 4-bit paged cache, in its plainest form: one block per (query token, query
-// head) walks the tokens it may see, 128 at a time, with the running maximum and sum of a softmax.
+// Attention over the 4-bit paged cache.
+//
+// The rows (query token, query head) that share a kv head are taken 8 or 16 at a time; such a row
+// block with the tokens that it may see is an item.  All items' tokens form one line that is cut
+// into equal ranges, a range to a warp: long contexts are split over many warps, short ones
+// share a warp, whatever the lengths.  A warp streams its units (16 tokens, keys and values
+// together: one bulk copy each) through a ring of its own in shared memory and waits for no other
+// warp.  Per unit, with codes c, steps s and zeros z:
+//   scores   S^T = sum_g s_g (C_g Q_g^T) + Z qsum^T    (16 tokens x 8 rows per product)
+//            4-bit codes are fp16 numbers as they stand: 0x000c is c 2^-24, a subnormal, and
+//            0x00c0 is 16 c 2^-24, so unpacking is one AND per pair; the 16 is taken out of q.
+//            Steps multiply in fp32 after the products, zeros enter as one more product with the
+//            groups' sums of q (in two fp16 parts), so scores carry no 16-bit rounding: q itself
+//            is scaled to fp16 by a power of two per row.
+//   softmax  base 2, against a running maximum that moves only when a score passes it by 8.
+//   values   O^T += V^T P^T with V = fp16(c s + z) and P in fp16, for fp16 outputs in two parts:
+//            one rounding of 2^-12 then, beside the output's own; bf16's own is 2^-9.
+// A warp's unfinished ranges are joined in shared memory, a block's in a second small kernel.
+//
+// mma.sync and not tcgen05: the products of decode are 8 to 16 rows wide, operands come out of
+// registers, and the tensor pipe has three quarters of its time left at the HBM bound.
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fq_internal.h"
 #include "kv4.h"
+#include "sm100_ptx.cuh"
 
 namespace fq {
 namespace kv4 {
 namespace {
 
-constexpr int kThreads = 128;
+__device__ unsigned int g_kv4_wait_timeouts = 0;  // blocks whose bounded waits gave up
 
-__device__ __forceinline__ float load_q(const void* q, fq_dtype t, int64_t i) {
-  return t == FQ_F16 ? __half2float(static_cast<const __half*>(q)[i])
-                     : __bfloat162float(static_cast<const __nv_bfloat16*>(q)[i]);
-}
+constexpr int kCtas = 148;       // one block per SM
+constexpr int kStages = 4;       // units of a warp's ring
+constexpr int kItemTokens = 48;  // an item's fixed cost, in tokens (its queries and its end)
 
-// The unit of token position `pos` of sequence b, or null when its page is not in the pool.
-__device__ __forceinline__ const uint8_t* unit_of(const AttnArgs& a, int b, int head, int pos) {
-  const int id = a.tables[(int64_t)b * a.max_blocks + pos / a.page];
-  if (id < 0 || id >= a.n_blocks) return nullptr;
-  return a.cache + (((int64_t)id * a.hkv + head) * (a.page / kUnit) + pos % a.page / kUnit) *
-                       unit_bytes(a.d, a.group);
-}
+template <int NT>
+constexpr int kWarpsOf = NT == 1 ? 16 : 12;
 
-__device__ float block_reduce(float x, bool is_max, float* part) {
-#pragma unroll
-  for (int m = 16; m; m >>= 1) {
-    const float y = __shfl_xor_sync(~0u, x, m);
-    x = is_max ? fmaxf(x, y) : x + y;
-  }
-  __syncthreads();
-  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = x;
-  __syncthreads();
-  x = part[0];
-  for (int i = 1; i < kThreads / 32; ++i) x = is_max ? fmaxf(x, part[i]) : x + part[i];
-  return x;
-}
+// What a block leaves for the second kernel: [kCtas][2] parts, part 0 of an item begun before the
+// block's range, part 1 of an item begun in it that goes on behind it.
+struct PartHeader {
+  int state;  // 0: none, 1: goes on, 3: the item's last part
+  int b, head, rb;
+};
+template <int NT, int D>
+struct Part {
+  float4 o[NT * D / 16 * 32];  // accumulators in fragment order
+  float m[8 * NT], l[8 * NT];
+};
 
-__global__ void __launch_bounds__(kThreads) attn_kernel(AttnArgs a) {
-  __shared__ float q[128], p[kThreads], part[4];
-  const int64_t row = blockIdx.x / a.hq;
-  const int h = blockIdx.x % a.hq, head = h / (a.hq / a.hkv), tid = threadIdx.x;
-  int b = (int)row, m = 1, i = 0;
-  if (a.cu_q) {
-    for (b = 0; b < a.B; ++b)
-      if (row >= a.cu_q[b] && row < a.cu_q[b + 1]) break;
-    if (b == a.B) return;  // a row behind the last sequence
-    m = a.cu_q[b + 1] - a.cu_q[b];
-    i = (int)(row - a.cu_q[b]);
-  }
+// ------------------------------------------------------------------------------ items
+
+struct Seq {
+  int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
+  int64_t k0;                  // cost of row block rb: k0 + slope (rb + 1), in 1 / (hq / hkv) tokens
+  int slope;
+  __device__ int64_t upto(int rb) const { return rb * k0 + (int64_t)slope * rb * (rb + 1) / 2; }
+};
+
+template <int NB>
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
+  Seq s;
   const int64_t room = (int64_t)a.max_blocks * a.page;
-  const int n = (int)min((int64_t)max(a.kv_lens[b], 0), room);
-  const int end = min(n, n - m + i + 1), first = a.window > 0 ? max(0, end - a.window) : 0;
-  for (int c = tid; c < a.d; c += kThreads) q[c] = load_q(a.q, a.type, row * a.q_tok + h * a.q_head + c);
-  __syncthreads();
-  const int ng = a.d / a.group;
-  float top = -INFINITY, sum = 0.f, acc = 0.f;
-  for (int t0 = first; t0 < end; t0 += kThreads) {
-    const int pos = t0 + tid, ut = pos % kUnit;
-    float s = -INFINITY;
-    const uint8_t* unit = pos < end ? unit_of(a, b, head, pos) : nullptr;
-    if (unit) {
-      const uint32_t* codes = reinterpret_cast<const uint32_t*>(unit) + key_row(ut) * (a.d / 8);
-      const __half* sz = reinterpret_cast<const __half*>(unit + off_ks(a.d)) + key_row(ut) * 2 * ng;
-      s = 0.f;
-      for (int w = 0; w < a.d / 8; ++w) {
-        const uint32_t word = codes[key_word(w, a.d)];
-        const int g = w * 8 / a.group;
-        const float step = __half2float(sz[g]), zero = __half2float(sz[ng + g]);
-        for (int e = 0; e < 8; ++e)
-          s += q[8 * w + e] * fmaf((float)((word >> (4 * e)) & 15), step, zero);
+  s.n = (int)min((int64_t)max(__ldg(a.kv_lens + b), 0), room);
+  s.q0 = b;
+  s.m = 1;
+  if (a.cu_q) {
+    s.q0 = __ldg(a.cu_q + b);
+    s.m = max(0, min(__ldg(a.cu_q + b + 1) - s.q0, a.max_q));
+    if (s.q0 < 0 || (int64_t)s.q0 + s.m > a.n_q) s.m = 0;
+  }
+  s.rows = s.m * r;
+  s.blocks = (s.rows + NB - 1) / NB;
+  // an upper bound of the tokens that each row block sees, linear in the row block
+  if (a.window > 0) {
+    s.k0 = (int64_t)r * (kItemTokens + 32 + min((int64_t)s.n, (int64_t)a.window + NB));
+    s.slope = 0;
+  } else {
+    s.k0 = (int64_t)r * (kItemTokens + 16 + max(s.n - s.m + 1, 0));
+    s.slope = NB;
+  }
+  return s;
+}
+
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) { return (a & b) | c; }
+
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+__device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                      uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* x) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[0]) : "r"(at));
+}
+
+// ------------------------------------------------------------------------------ one warp's state
+
+template <typename T>
+__device__ __forceinline__ float q_float(uint16_t x) {
+  if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) return __uint_as_float((uint32_t)x << 16);
+  else return __half2float(__ushort_as_half(x));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (__is_same(T, __half)) {
+    return u32(__floats2half2_rn(a, b));
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+template <typename T, int D, int G, int NT>
+struct Warp {
+  static constexpr int NG = D / G, KB = D / 32, MT = D / 16, UB = kUnit * D + 128 * NG;
+  static constexpr bool kTwoParts = __is_same(T, __half);
+  uint32_t q[NT][KB][4];     // query fragments; odd ones over 16
+  uint32_t qz[NT][2];        // sums of q over the groups, two parts (the second word for NG = 8 only)
+  float kappa[NT][2];        // score scale of rows 2 t, 2 t + 1 of the tile
+  int hi[NT][2], lo[NT][2];  // tokens that the rows see: [lo, hi)
+  float o[NT][MT][4], m[NT][2], l[NT][2];
+
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.f;
+      m[nt][0] = m[nt][1] = -FLT_MAX;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+  }
+
+  // Queries of row block rb of (sequence, kv head): row r is query token r / R, head r % R.
+  __device__ __forceinline__ void load_queries(const AttnArgs& a, const Seq& s, int head, int rb, int r, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    const int past = s.n - s.m + 1;
+    float kap[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = rb * 8 * NT + nt * 8 + g;
+      const bool in = row < s.rows;
+      const int tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(s.q0 + tok) * a.q_tok +
+                            (int64_t)(head * r + hh) * a.q_head + 8 * t;
+      const bool wide = in && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+      float x[KB][8];
+      float top = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        uint16_t w[8];
+        if (wide) {
+          *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(src + 32 * kb));
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = in ? __ldg(src + 32 * kb + e) : 0;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[kb][e] = q_float<T>(w[e]);
+          top = fmaxf(top, fabsf(x[kb][e]));
+        }
       }
-      s *= a.scale;
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+      // the row times 2^-e lies within +-2^8: exact in fp16 but for what is 2^-28 of the largest
+      int e = top > 0.f ? (int)(__float_as_uint(top) >> 23) - 127 - 7 : 0;
+      e = max(e, -126);
+      const float down = __uint_as_float((uint32_t)(127 - max(e, -126)) << 23);
+      kap[nt] = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+      float sum[NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) sum[i] = 0.f;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        __half y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          y[i] = __float2half_rn(x[kb][i] * down);
+          sum[32 * kb / G] += __half2float(y[i]);
+        }
+        const __half2 over = __floats2half2_rn(0.0625f, 0.0625f);
+        q[nt][kb][0] = u32(__halves2half2(y[0], y[4]));
+        q[nt][kb][1] = u32(__hmul2(__halves2half2(y[1], y[5]), over));
+        q[nt][kb][2] = u32(__halves2half2(y[2], y[6]));
+        q[nt][kb][3] = u32(__hmul2(__halves2half2(y[3], y[7]), over));
+      }
+      __half part[2][NG];
+#pragma unroll
+      for (int i = 0; i < NG; ++i) {
+        sum[i] += __shfl_xor_sync(~0u, sum[i], 1);
+        sum[i] += __shfl_xor_sync(~0u, sum[i], 2);
+        part[0][i] = __float2half_rn(sum[i]);
+        part[1][i] = __float2half_rn(sum[i] - __half2float(part[0][i]));
+      }
+      // zero words of a token: (z0 z1) (z2 z3) for NG = 4, (z0 z1) for 2, (s0 z0) for 1
+      const __half none = __ushort_as_half(0);
+      uint32_t w = 0;
+      if constexpr (NG == 4) {
+        const int p = t >> 1;
+        w = t & 1 ? u32(__halves2half2(part[p][2], part[p][3])) : u32(__halves2half2(part[p][0], part[p][1]));
+      } else if constexpr (NG == 2) {
+        if (t < 2) w = u32(__halves2half2(part[t][0], part[t][1]));
+      } else {
+        if (t < 2) w = u32(__halves2half2(none, part[t][0]));
+      }
+      qz[nt][0] = w;
     }
-    const float now = fmaxf(top, block_reduce(s, true, part));
-    const float base = now == -INFINITY ? 0.f : now;
-    const float keep = expf(top - base);
-    p[tid] = expf(s - base);
-    sum = sum * keep + block_reduce(p[tid], false, part);  // its barriers publish p
-    acc *= keep;
-    top = now;
-    for (int j = 0; j < kThreads && t0 + j < end; ++j) {
-      if (p[j] == 0.f || tid >= a.d) continue;  // a masked token's codes and steps may hold anything
-      const uint8_t* u = unit_of(a, b, head, t0 + j);
-      const int tt = (t0 + j) % kUnit;
-      const uint32_t word = reinterpret_cast<const uint32_t*>(u + off_v(a.d))[tt * (a.d / 8) + value_word(tid / 8, tt, a.d)];
-      const __half* sz = reinterpret_cast<const __half*>(u + off_vs(a.d, a.group)) + (tt * ng + tid / a.group) * 2;
-      acc += p[j] * fmaf((float)((word >> (4 * (tid % 8))) & 15), __half2float(sz[0]), __half2float(sz[1]));
+    // the accumulators' columns are rows 2 t, 2 t + 1: their scale sits in lanes 8 t, 8 t + 4
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        kappa[nt][c] = __shfl_sync(~0u, kap[nt], 8 * t + 4 * c);
+        const int row = min(rb * 8 * NT + nt * 8 + 2 * t + c, s.rows - 1);
+        hi[nt][c] = past + row / r;
+        lo[nt][c] = a.window > 0 ? hi[nt][c] - a.window : 0;
+      }
+  }
+
+  // One unit at shared address `u`, whose first token is at position pos0.  MASK: some row does not
+  // see all of it; [first, end) is what any row sees.
+  template <bool MASK>
+  __device__ __forceinline__ void unit(uint32_t u, int pos0, int first, int end, int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    uint32_t k0[KB], k1[KB];
+    lds<D / 8>(u + lane * (D / 8), k0);
+    lds<D / 8>(u + lane * (D / 8) + 4 * D, k1);
+    // steps of token rows g and g + 8, and the zero words that this lane feeds to the product
+    uint32_t s0[(NG + 1) / 2], s1[(NG + 1) / 2], z0, z1;
+    const uint32_t ks = u + off_ks(D) + g * 4 * NG;
+    if constexpr (NG == 1) {
+      lds<4>(ks, s0);
+      lds<4>(ks + 32, s1);
+      z0 = s0[0];
+      z1 = s1[0];
+    } else {
+      lds<2 * NG>(ks, s0);
+      lds<2 * NG>(ks + 32 * NG, s1);
+      const uint32_t zw = ks + 2 * NG + 4 * (t & (NG / 2 - 1));
+      lds<4>(zw, &z0);
+      lds<4>(zw + 32 * NG, &z1);
     }
-    __syncthreads();
+    float x[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+      float acc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+#pragma unroll
+      for (int kb = gr * G / 32; kb < (gr + 1) * G / 32; ++kb) {
+        const uint32_t lowm = 0x000F000Fu, highm = 0x00F000F0u;
+        const uint32_t a = k0[kb] >> 8, b = k1[kb] >> 8;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16(acc[nt], k0[kb] & lowm, k1[kb] & lowm, k0[kb] & highm, k1[kb] & highm, q[nt][kb][0], q[nt][kb][1]);
+          mma16(acc[nt], a & lowm, b & lowm, a & highm, b & highm, q[nt][kb][2], q[nt][kb][3]);
+        }
+      }
+      const __half2 p0 = h2(s0[gr / 2]), p1 = h2(s1[gr / 2]);
+      const float f0 = gr % 2 ? __high2float(p0) : __low2float(p0);
+      const float f1 = gr % 2 ? __high2float(p1) : __low2float(p1);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        x[nt][0] = fmaf(acc[nt][0], f0, x[nt][0]);
+        x[nt][1] = fmaf(acc[nt][1], f0, x[nt][1]);
+        x[nt][2] = fmaf(acc[nt][2], f1, x[nt][2]);
+        x[nt][3] = fmaf(acc[nt][3], f1, x[nt][3]);
+      }
+    }
+    bool passes = false;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      mma8(acc, z0, z1, qz[nt][0]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[nt][i] = fmaf(x[nt][i], 16777216.f, acc[i]) * kappa[nt][i & 1];
+        if (MASK) {
+          // rows of the product are tokens (g >> 1) + 4 (g & 1), and 8 further
+          const int pos = pos0 + (g >> 1) + 4 * (g & 1) + 4 * (i & 2);
+          if (pos >= hi[nt][i & 1] || pos < lo[nt][i & 1]) x[nt][i] = -INFINITY;
+        }
+        passes |= x[nt][i] > m[nt][i & 1] + 8.f;
+      }
+    }
+    if (__any_sync(~0u, passes)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = fmaxf(x[nt][c], x[nt][c + 2]);
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
+          top = fmaxf(top, m[nt][c]);
+          const float f = ex2(m[nt][c] - top);
+          m[nt][c] = top;
+          l[nt][c] *= f;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            o[nt][mt][c] *= f;
+            o[nt][mt][c + 2] *= f;
+          }
+        }
+    }
+    uint32_t p[NT][2], pl[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[nt][i] = ex2(x[nt][i] - m[nt][i & 1]);
+      l[nt][0] += x[nt][0] + x[nt][2];
+      l[nt][1] += x[nt][1] + x[nt][3];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const __half2 v = __floats2half2_rn(x[nt][2 * i], x[nt][2 * i + 1]);
+        p[nt][i] = transpose8(u32(v));
+        if (kTwoParts) {
+          const float2 f = __half22float2(v);
+          pl[nt][i] = transpose8(u32(__floats2half2_rn(x[nt][2 * i] - f.x, x[nt][2 * i + 1] - f.y)));
+        }
+      }
+    }
+    // values: this lane's tokens are t + 4 i, its coordinates g D/8 .. + D/8 (all of one group)
+    uint32_t w[4][D / 64], sz[4];
+    const uint32_t vb = u + off_v(D) + (D == 128 ? ((2 * g) ^ ((t & 2) << 2)) * 4 : 4 * g);
+    const uint32_t vs = u + off_vs(D, G) + t * 4 * NG + (g * (D / 8) / G) * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lds<D / 16>(vb + (t + 4 * i) * (D / 2), w[i]);
+      lds<4>(vs + 16 * i * NG, &sz[i]);
+      if (MASK) {
+        const int pos = pos0 + t + 4 * i;
+        if (pos < first || pos >= end) sz[i] = 0;  // a token that nobody sees: its value becomes 0
+      }
+    }
+    const __half2 st[2] = {h2(__byte_perm(sz[0], sz[1], 0x5410)), h2(__byte_perm(sz[2], sz[3], 0x5410))};
+    const __half2 ze[2] = {h2(__byte_perm(sz[0], sz[1], 0x7632)), h2(__byte_perm(sz[2], sz[3], 0x7632))};
+    const __half2 bias = h2(0xE400E400u), sixteenth = h2(0x2C002C00u), bias16 = h2(0xD400D400u);
+#pragma unroll
+    for (int wi = 0; wi < D / 64; ++wi)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t v[2][4];  // [token pair][coordinate]
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t y = __byte_perm(w[2 * j][wi], w[2 * j + 1][wi], half ? 0x7632 : 0x5410);
+          const uint32_t y8 = y >> 8;
+          // 0x6400 + c is 1024 + c, 0x6400 + 16 c is 1024 + 16 c: back to c without rounding
+          const __half2 c0 = __hadd2(h2(and_or(y, 0x000F000Fu, 0x64006400u)), bias);
+          const __half2 c1 = __hfma2(h2(and_or(y, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+          const __half2 c2 = __hadd2(h2(and_or(y8, 0x000F000Fu, 0x64006400u)), bias);
+          const __half2 c3 = __hfma2(h2(and_or(y8, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+          v[j][0] = u32(__hfma2(c0, st[j], ze[j]));
+          v[j][1] = u32(__hfma2(c1, st[j], ze[j]));
+          v[j][2] = u32(__hfma2(c2, st[j], ze[j]));
+          v[j][3] = u32(__hfma2(c3, st[j], ze[j]));
+        }
+        const int mt = wi * 4 + half * 2;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma16(o[nt][mt], v[0][0], v[0][1], v[1][0], v[1][1], p[nt][0], p[nt][1]);
+          mma16(o[nt][mt + 1], v[0][2], v[0][3], v[1][2], v[1][3], p[nt][0], p[nt][1]);
+          if (kTwoParts) {
+            mma16(o[nt][mt], v[0][0], v[0][1], v[1][0], v[1][1], pl[nt][0], pl[nt][1]);
+            mma16(o[nt][mt + 1], v[0][2], v[0][3], v[1][2], v[1][3], pl[nt][0], pl[nt][1]);
+          }
+        }
+      }
   }
-  if (tid < a.d) {
-    const float o = sum > 0.f ? acc / sum : 0.f;
-    const int64_t at = (row * a.hq + h) * a.d + tid;
-    if (a.type == FQ_F16) static_cast<__half*>(a.out)[at] = __float2half_rn(o);
-    else static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
+
+  __device__ __forceinline__ void finish_sums() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], d);
   }
+
+  __device__ __forceinline__ void write_part(Part<NT, D>* part, int lane) const {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+        part->o[(nt * MT + mt) * 32 + lane] = make_float4(o[nt][mt][0], o[nt][mt][1], o[nt][mt][2], o[nt][mt][3]);
+      if (lane < 4) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          part->m[nt * 8 + 2 * lane + c] = m[nt][c];
+          part->l[nt * 8 + 2 * lane + c] = l[nt][c];
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void write_out(const AttnArgs& a, const Seq& s, int head, int rb, int r, int lane) const {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = rb * 8 * NT + nt * 8 + 2 * t + c;
+        if (row >= s.rows) continue;
+        const int tok = row / r;
+        const float inv = l[nt][c] > 0.f ? 1.0f / l[nt][c] : 0.f;
+        T* dst = static_cast<T*>(a.out) + ((int64_t)(s.q0 + tok) * a.hq + head * r + row - tok * r) * D + g * (D / 8);
+#pragma unroll
+        for (int i = 0; i < MT / 4; ++i) {
+          uint4 v;
+          v.x = pack_out<T>(o[nt][4 * i][c] * inv, o[nt][4 * i][c + 2] * inv);
+          v.y = pack_out<T>(o[nt][4 * i + 1][c] * inv, o[nt][4 * i + 1][c + 2] * inv);
+          v.z = pack_out<T>(o[nt][4 * i + 2][c] * inv, o[nt][4 * i + 2][c + 2] * inv);
+          v.w = pack_out<T>(o[nt][4 * i + 3][c] * inv, o[nt][4 * i + 3][c + 2] * inv);
+          reinterpret_cast<uint4*>(dst)[i] = v;
+        }
+      }
+  }
+};
+
+// Merged accumulators of one fragment word of an item into out: rows 2 t and 2 t + 1, two coordinates.
+template <typename T, int D, int NT>
+__device__ __forceinline__ void write_merged(const AttnArgs& a, int b, int head, int rb, int e, float4 o, float l0, float l1) {
+  const int lane = e & 31, mt = (e >> 5) % (D / 16), nt = (e >> 5) / (D / 16), g = lane >> 2, t = lane & 3;
+  const int r = a.hq / a.hkv;
+  const Seq s = load_seq<8 * NT>(a, b, r);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int row = rb * 8 * NT + nt * 8 + 2 * t + c;
+    if (row >= s.rows) continue;
+    const int tok = row / r;
+    const float l = c ? l1 : l0, inv = l > 0.f ? 1.0f / l : 0.f;
+    T* dst = static_cast<T*>(a.out) + ((int64_t)(s.q0 + tok) * a.hq + head * r + row - tok * r) * D + g * (D / 8) + 2 * mt;
+    *reinterpret_cast<uint32_t*>(dst) = pack_out<T>((c ? o.y : o.x) * inv, (c ? o.w : o.z) * inv);
+  }
+}
+
+template <typename T, int D, int G, int NT>
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift) {
+  using W_ = Warp<T, D, G, NT>;
+  using P = Part<NT, D>;
+  constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB;
+  constexpr size_t kSlot = kStages * UB > (int)sizeof(P) ? kStages * UB : sizeof(P);
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* rings = smem;                                          // [W][kSlot]
+  P* heads = reinterpret_cast<P*>(smem + W * kSlot);              // [W]
+  __shared__ uint64_t bars[W][kStages];
+  __shared__ PartHeader hdr[W][2];
+  __shared__ int64_t scan[W];
+  __shared__ int gave_up;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = a.hq / a.hkv;
+
+  if (tid == 0) gave_up = 0;
+  if (lane < kStages) ptx::mbar_init(&bars[warp][lane], 1);
+  if (lane < 2) hdr[warp][lane].state = 0;
+  ptx::fence_mbar_init();
+
+  // sums of the sequences' costs, in shared memory (where the rings will be)
+  int64_t* sums = reinterpret_cast<int64_t*>(smem);
+  const int per = (a.B + 32 * W - 1) / (32 * W);
+  int64_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int b = tid * per + i;
+    if (b < a.B) {
+      const Seq s = load_seq<NB>(a, b, r);
+      mine += a.hkv * s.upto(s.blocks);
+      sums[b] = mine;
+    }
+  }
+  int64_t x = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t y = __shfl_up_sync(~0u, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) scan[warp] = x;
+  __syncthreads();
+  int64_t below = x - mine, total = 0;
+  for (int w = 0; w < W; ++w) {
+    if (w < warp) below += scan[w];
+    total += scan[w];
+  }
+  for (int i = 0; i < per; ++i)
+    if (tid * per + i < a.B) sums[tid * per + i] += below;
+  ptx::fence_proxy_async_smem();  // copies will write where the sums are
+  __syncthreads();
+
+  // this warp's range of the line, at least a unit long
+  const int64_t span = max((total + kCtas * W - 1) / (kCtas * W), (int64_t)kUnit * r);
+  const int64_t x0 = (int64_t)(blockIdx.x * W + warp) * span, x1 = min(total, x0 + span);
+  int b = 0;
+  int64_t base = 0;
+  if (x0 < x1) {
+    int lo = 0, hi = a.B - 1;  // the first sequence whose sum is past x0
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (sums[mid] > x0) hi = mid; else lo = mid + 1;
+    }
+    b = lo;
+    base = b > 0 ? sums[b - 1] : 0;
+  }
+  __syncthreads();
+
+  W_ st;
+  uint8_t* ring = rings + warp * kSlot;
+  const uint32_t ring32 = ptx::smem_u32(ring);
+  int stage = 0;
+  uint32_t phase = 0;
+  bool ok = true;
+  int64_t at = x0;
+  while (at < x1 && ok) {
+    // the item at `at`
+    const Seq s = load_seq<NB>(a, b, r);
+    const int64_t one = s.upto(s.blocks), in_seq = at - base;
+    if (in_seq >= a.hkv * one) {
+      base += a.hkv * one;
+      ++b;
+      continue;
+    }
+    const int head = (int)(in_seq / one);
+    const int64_t in_head = in_seq - head * one;
+    int rb = 0, above = s.blocks;
+    while (above - rb > 1) {
+      const int mid = (rb + above) >> 1;
+      if (s.upto(mid) <= in_head) rb = mid; else above = mid;
+    }
+    const int64_t item0 = base + head * one + s.upto(rb), cost = s.upto(rb + 1) - s.upto(rb);
+    const int64_t from = at - item0, to = min(x1 - item0, cost);
+    at = item0 + to;
+    // tokens that any row of the block sees, in units; the part of them in this range
+    const int past = s.n - s.m + 1, row0 = rb * NB, row1 = min(row0 + NB, s.rows) - 1;
+    const int end = max(0, past + row1 / r);
+    const int first = a.window > 0 ? max(0, past + row0 / r - a.window) : 0;
+    const int base_u = first / kUnit, units = end > first ? (end + kUnit - 1) / kUnit - base_u : 0;
+    const int64_t fixed = (int64_t)kItemTokens * r, step = (int64_t)kUnit * r;
+    const int u0 = from <= fixed ? 0 : (int)min((int64_t)units, (from - fixed + step - 1) / step);
+    const int u1 = to == cost ? units : to <= fixed ? 0 : (int)min((int64_t)units, (to - fixed + step - 1) / step);
+
+    st.reset();
+    if (u0 < u1) {
+      // Copies run kStages units ahead; lane i issues units i, i + 32, ... of the range, from the
+      // table entry that it holds.  A unit on a page outside the pool is neither copied nor used.
+      const int32_t* table = a.tables + (int64_t)b * a.max_blocks;
+      const int unit_mask = (1 << (page_shift - 4)) - 1;
+      auto entry = [&](int i) {
+        const int u = base_u + i;
+        return i < u1 ? __ldg(table + (u >> (page_shift - 4))) : -1;
+      };
+      int id = entry(u0 + lane), id_next = entry(u0 + 32 + lane);
+      uint32_t there = 0;  // of the last 32 units that were issued (bit: unit mod 32)
+      int put_stage = stage;
+      auto issue = [&](int i) {
+        const int who = (i - u0) & 31;
+        if (who == 0 && i != u0) {
+          id = id_next;
+          id_next = entry(i + 32 + lane);
+        }
+        const bool good = id >= 0 && id < a.n_blocks;
+        const uint32_t all = __ballot_sync(~0u, good);
+        const bool has = (all >> who) & 1;
+        there = (there & ~(1u << who)) | ((uint32_t)has << who);
+        if (has) {
+          if (lane == who) {
+            const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + head) << (page_shift - 4)) + ((base_u + i) & unit_mask)) * UB;
+            ptx::mbar_arrive_expect_tx(&bars[warp][put_stage], UB);
+            ptx::bulk_load(ring + put_stage * UB, src, UB, &bars[warp][put_stage]);
+          }
+          put_stage = put_stage + 1 == kStages ? 0 : put_stage + 1;
+        }
+      };
+      // units issued and not used are at most kStages
+      int put = u0;
+      for (; put < u1 && put < u0 + kStages; ++put) issue(put);
+      st.load_queries(a, s, head, rb, r, lane);
+      const int all_end = past + row0 / r, all_first = a.window > 0 ? past + row1 / r - a.window : 0;
+      // a wait that gives up ends the loop once the copies in flight had their time to land
+      for (int i = u0; i < u1 && (ok || i < put); ++i) {
+        if ((there >> ((i - u0) & 31)) & 1) {
+          ok = __all_sync(~0u, ptx::mbar_wait(&bars[warp][stage], (phase >> stage) & 1)) && ok;
+          phase ^= 1u << stage;
+          if (ok) {
+            const int pos0 = (base_u + i) * kUnit;
+            const uint32_t u = ring32 + stage * UB;
+            if (pos0 >= all_first && pos0 + kUnit <= all_end) st.template unit<false>(u, pos0, first, end, lane);
+            else st.template unit<true>(u, pos0, first, end, lane);
+          }
+          stage = stage + 1 == kStages ? 0 : stage + 1;
+          __syncwarp();
+        }
+        if (put < u1 && ok) issue(put++);
+      }
+      st.finish_sums();
+    }
+    if (from == 0 && to == cost) {
+      st.write_out(a, s, head, rb, r, lane);
+    } else {
+      // an item begun before this range leaves its part beside the ring, one that goes on in it
+      const int k = from > 0 ? 0 : 1;
+      st.write_part(k == 0 ? heads + warp : reinterpret_cast<P*>(ring), lane);
+      if (lane == 0) hdr[warp][k] = PartHeader{to == cost ? 3 : 1, b, head, rb};
+    }
+  }
+  if (!ok) gave_up = 1;
+  __syncthreads();
+  if (tid == 0 && gave_up) atomicAdd(&g_kv4_wait_timeouts, 1u);
+
+  // Join the parts of each item, in order; what begins before or ends behind the block goes to the
+  // workspace.
+  PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
+  P* out_part = reinterpret_cast<P*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
+  bool left[2] = {false, false};
+  auto part_of = [&](int i) -> const P& {
+    return (i & 1) ? *reinterpret_cast<const P*>(rings + (i >> 1) * kSlot) : heads[i >> 1];
+  };
+  for (int i = 0; i < 2 * W;) {
+    const PartHeader h = hdr[i >> 1][i & 1];
+    if (h.state == 0) { ++i; continue; }
+    // parts i, then the next warps' parts 0, until the item's last one
+    int count = 1, last = h.state;
+    const bool begun = i & 1;
+    for (int j = (i >> 1) + 1; last == 1 && j < W && hdr[j][0].state != 0; ++j) {
+      last = hdr[j][0].state;
+      ++count;
+    }
+    const bool whole = begun && last == 3;
+    const int k = begun ? 1 : 0;
+    P* dst = out_part + blockIdx.x * 2 + k;
+    for (int e = tid; e < NT * W_::MT * 32; e += 32 * W) {
+      const int lane_e = e & 31, row = ((e >> 5) / W_::MT) * 8 + 2 * (lane_e & 3);
+      float m0 = -FLT_MAX, m1 = -FLT_MAX;
+      for (int c = 0; c < count; ++c) {
+        const P& p = part_of(c == 0 ? i : ((i >> 1) + c) * 2);
+        m0 = fmaxf(m0, p.m[row]);
+        m1 = fmaxf(m1, p.m[row + 1]);
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float l0 = 0.f, l1 = 0.f;
+      for (int c = 0; c < count; ++c) {
+        const P& p = part_of(c == 0 ? i : ((i >> 1) + c) * 2);
+        const float f0 = ex2(p.m[row] - m0), f1 = ex2(p.m[row + 1] - m1);
+        const float4 y = p.o[e];
+        o.x = fmaf(y.x, f0, o.x);
+        o.y = fmaf(y.y, f1, o.y);
+        o.z = fmaf(y.z, f0, o.z);
+        o.w = fmaf(y.w, f1, o.w);
+        l0 = fmaf(p.l[row], f0, l0);
+        l1 = fmaf(p.l[row + 1], f1, l1);
+      }
+      if (whole) {
+        write_merged<T, D, NT>(a, h.b, h.head, h.rb, e, o, l0, l1);
+      } else {
+        dst->o[e] = o;
+        if (((e >> 5) % W_::MT) == 0 && lane_e < 4) {
+          dst->m[row] = m0;
+          dst->m[row + 1] = m1;
+          dst->l[row] = l0;
+          dst->l[row + 1] = l1;
+        }
+      }
+    }
+    if (!whole) {
+      left[k] = true;
+      if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{last, h.b, h.head, h.rb};
+    }
+    // on to the last of these warps' part 1, which may begin another item
+    i += begun ? max(1, 2 * count - 2) : 2 * count - 1;
+  }
+  if (tid < 2 && !left[tid]) out_hdr[blockIdx.x * 2 + tid].state = 0;
+}
+
+// Joins the parts of the items that span blocks: block c those of the item begun in block c of the
+// first kernel.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
+  using P = Part<NT, D>;
+  const PartHeader* hdr = static_cast<const PartHeader*>(a.workspace);
+  const P* part = reinterpret_cast<const P*>(static_cast<const uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
+  const int c0 = blockIdx.x;
+  const PartHeader h = hdr[c0 * 2 + 1];
+  if (h.state != 1) return;
+  __shared__ int last;
+  if (threadIdx.x == 0) last = kCtas - 1;
+  __syncthreads();
+  for (int c = c0 + 1 + threadIdx.x; c < kCtas; c += blockDim.x)
+    if (hdr[c * 2].state == 3) atomicMin(&last, c);
+  __syncthreads();
+  const int end = last;
+  for (int e = threadIdx.x; e < NT * D / 16 * 32; e += blockDim.x) {
+    const int row = ((e >> 5) / (D / 16)) * 8 + 2 * (e & 3);
+    const P* p0 = part + c0 * 2 + 1;
+    float m0 = p0->m[row], m1 = p0->m[row + 1];
+    for (int c = c0 + 1; c <= end; ++c) {
+      m0 = fmaxf(m0, part[c * 2].m[row]);
+      m1 = fmaxf(m1, part[c * 2].m[row + 1]);
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l0 = 0.f, l1 = 0.f;
+    for (int c = c0; c <= end; ++c) {
+      const P& p = c == c0 ? *p0 : part[c * 2];
+      const float f0 = ex2(p.m[row] - m0), f1 = ex2(p.m[row + 1] - m1);
+      const float4 y = p.o[e];
+      o.x = fmaf(y.x, f0, o.x);
+      o.y = fmaf(y.y, f1, o.y);
+      o.z = fmaf(y.z, f0, o.z);
+      o.w = fmaf(y.w, f1, o.w);
+      l0 = fmaf(p.l[row], f0, l0);
+      l1 = fmaf(p.l[row + 1], f1, l1);
+    }
+    write_merged<T, D, NT>(a, h.b, h.head, h.rb, e, o, l0, l1);
+  }
+}
+
+template <typename T, int D, int G, int NT>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  using P = Part<NT, D>;
+  constexpr int W = kWarpsOf<NT>, UB = unit_bytes(D, G);
+  constexpr size_t slot = kStages * UB > (int)sizeof(P) ? kStages * UB : sizeof(P);
+  constexpr size_t rings = W * (slot + sizeof(P)), table = sizeof(int64_t) * kMaxRequests;
+  constexpr size_t bytes = rings > table ? rings : table;
+  static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
+  static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0, "parts are read in 16 bytes");
+  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  int shift = 4;
+  while ((1 << shift) < a.page) ++shift;
+  attn_kernel<T, D, G, NT><<<kCtas, 32 * W, bytes, st>>>(a, shift);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  combine_kernel<T, D, NT><<<kCtas, 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <typename T, int D, int G>
+cudaError_t launch_rows(const AttnArgs& a, cudaStream_t st) {
+  // 8 rows a block while a kv head has no more: half the products and registers of 16
+  return (int64_t)a.max_q * (a.hq / a.hkv) <= 8 ? launch<T, D, G, 1>(a, st) : launch<T, D, G, 2>(a, st);
+}
+
+template <typename T>
+cudaError_t launch_shape(const AttnArgs& a, cudaStream_t st) {
+  if (a.d == 64) return a.group == 32 ? launch_rows<T, 64, 32>(a, st) : launch_rows<T, 64, 64>(a, st);
+  if (a.group == 32) return launch_rows<T, 128, 32>(a, st);
+  return a.group == 64 ? launch_rows<T, 128, 64>(a, st) : launch_rows<T, 128, 128>(a, st);
 }
 
 }  // namespace
 
-size_t attn_workspace_bytes(int) { return 16; }
+size_t attn_workspace_bytes(int d) {
+  return 2 * kCtas * (sizeof(PartHeader) + (d == 64 ? sizeof(Part<2, 64>) : sizeof(Part<2, 128>)));
+}
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
-  attn_kernel<<<(unsigned)(a.n_q * a.hq), kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return a.type == FQ_F16 ? launch_shape<__half>(a, st) : launch_shape<__nv_bfloat16>(a, st);
+}
+
+cudaError_t wait_timeouts_kv4(bool clear, unsigned* count) {
+  return read_wait_counter(g_kv4_wait_timeouts, clear, count);
 }
 
 }  // namespace kv4
