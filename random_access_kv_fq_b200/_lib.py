@@ -380,71 +380,89 @@ def fq_build_search_index(codebook, d: int, k: int, N: int, kind: int, L: int,
 
 # ---- the 4-bit paged cache ---------------------------------------------------------------------
 
-def _kv4_dtype(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return FQ_BF16
-    return _dtype_code(t)
+# These calls take microseconds of GPU time, so the checks below are kept to cheap attribute reads.
+
+_KV4_UNITS = {}   # (d, group) -> unit bytes
+_KV4_WS = {}      # d -> workspace bytes
 
 
-def _same_device(*tensors):
-    """The CUDA device that all tensors (None among them is skipped) are on."""
-    dev = None
+def _device_index(*tensors) -> int:
+    """The index of the CUDA device that all tensors (None among them is skipped) are on."""
+    dev = tensors[0].get_device()
     for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("expected CUDA tensors")
-        if dev is not None and t.device != dev:
-            raise ValueError(f"tensors on {dev} and {t.device}")
-        dev = t.device
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices")
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
     return dev
 
 
-class _On:
-    """Device and stream of a call: inside the block they are current, so that what the call
-    allocates belongs to the stream that uses it."""
+class _OnStream:
+    """Makes a stream and its device current, so that what a call allocates belongs to the stream
+    that uses it.  Entered, it gives the raw stream."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device: int, stream):
         import torch
-        if isinstance(stream, int):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        elif isinstance(stream, int):
             # 0 is the legacy default stream, which torch knows as its default stream
             stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                       else torch.cuda.default_stream(device))
-        elif stream is None:
-            stream = torch.cuda.current_stream(device)
-        if stream.device != device:
-            raise ValueError(f"stream of {stream.device} for tensors on {device}")
-        self._ctx = torch.cuda.stream(stream)
-        self.stream = stream.cuda_stream
+        if stream.device.index != device:
+            raise ValueError(f"a stream of {stream.device} for tensors on device {device}")
+        self._ctx, self._raw = torch.cuda.stream(stream), stream.cuda_stream
 
     def __enter__(self):
         self._ctx.__enter__()
-        return self.stream
+        return self._raw
 
     def __exit__(self, *exc):
         return self._ctx.__exit__(*exc)
 
 
-def _int32(name, t, shape=None):
+class _OnCurrent:
+    """The same where stream and device are current already."""
+
+    def __enter__(self):
+        return self._raw
+
+    def __exit__(self, *exc):
+        return None
+
+
+def _on(device: int, stream):
     import torch
-    if t.dtype != torch.int32 or not t.is_contiguous():
+    if stream is None and device == torch.cuda.current_device():
+        on = _OnCurrent()
+        on._raw = torch._C._cuda_getCurrentRawStream(device)
+        return on
+    return _OnStream(device, stream)
+
+
+def _int32(name, t, shape):
+    import torch
+    if t.dtype is not torch.int32 or not t.is_contiguous():
         raise TypeError(f"{name}: a contiguous int32 tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _kv4_cache(cache, d: int, group: int):
     """(n_blocks, Hkv, page) of a cache tensor [n_blocks, Hkv, page / 16, unit bytes]."""
     import torch
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
+    if cache.dtype is not torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
         raise TypeError("cache: a contiguous uint8 tensor [n_blocks, Hkv, page / 16, unit bytes]")
-    unit = fq_kv4_unit_bytes(d, group)
-    if unit == 0:
-        raise FQError("fq_kv4_unit_bytes", 2)
-    if cache.shape[3] != unit:
-        raise ValueError(f"cache: units of {cache.shape[3]} bytes, expected {unit}")
-    return cache.shape[0], cache.shape[1], 16 * cache.shape[2]
+    unit = _KV4_UNITS.get((d, group))
+    if unit is None:
+        unit = fq_kv4_unit_bytes(d, group)
+        if unit == 0:
+            raise FQError("fq_kv4_unit_bytes", 2)
+        _KV4_UNITS[d, group] = unit
+    n_blocks, hkv, units, size = cache.shape
+    if size != unit:
+        raise ValueError(f"cache: units of {size} bytes, expected {unit}")
+    return n_blocks, hkv, 16 * units
 
 
 def fq_kv4_unit_bytes(d: int, group: int) -> int:
@@ -462,32 +480,44 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
     free_list[:free_count]; tables and free list are updated in place, free_count too unless
     free_count_out is given.  Returns (lens_out [B], cu_new [B + 1], slots [n_slots], refused [1])."""
     import torch
-    dev = _same_device(lens, new_lens, block_tables, free_list, free_count, lens_out,
-                       free_count_out)
+    dev = _device_index(lens, new_lens, block_tables, free_list, free_count, lens_out,
+                        free_count_out)
     B = lens.numel()
     _int32("lens", lens, (B,))
     _int32("new_lens", new_lens, (B,))
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
+    if block_tables.dim() != 2:
         raise ValueError("block_tables: [B, max_blocks]")
-    _int32("block_tables", block_tables)
-    _int32("free_list", free_list, (free_list.numel(),))
+    max_blocks = block_tables.shape[1]
+    _int32("block_tables", block_tables, (B, max_blocks))
+    n_blocks = free_list.numel()
+    _int32("free_list", free_list, (n_blocks,))
     _int32("free_count", free_count, (1,))
+    if n_slots < 0:
+        raise ValueError("n_slots: at least 0")
     if free_count_out is None:
         free_count_out = free_count
-    _int32("free_count_out", free_count_out, (1,))
-    with _On(dev, stream) as s:
+    else:
+        _int32("free_count_out", free_count_out, (1,))
+    with _on(dev, stream) as s:
         if lens_out is None:
-            lens_out = torch.empty((B,), dtype=torch.int32, device=dev)
-        _int32("lens_out", lens_out, (B,))
-        cu_new = torch.empty((B + 1,), dtype=torch.int32, device=dev)
-        slots = torch.empty((max(n_slots, 0),), dtype=torch.int32, device=dev)
-        refused = torch.empty((1,), dtype=torch.int32, device=dev)
-        st = lib().fq_page_step(_ptr(lens), _ptr(new_lens), B, _ptr(block_tables),
-                                block_tables.shape[1], page, _ptr(free_list), free_list.numel(),
-                                _ptr(free_count), _ptr(lens_out), _ptr(free_count_out),
-                                _ptr(cu_new), _ptr(slots), n_slots, _ptr(refused), s)
-    _check("fq_page_step", st)
+            lens_out = lens.new_empty((B,))
+        else:
+            _int32("lens_out", lens_out, (B,))
+        # cu_new, refused and slots in one allocation
+        cu_new, refused, slots = lens.new_empty((B + 2 + n_slots,)).split((B + 1, 1, n_slots))
+        st = lib().fq_page_step(lens.data_ptr(), new_lens.data_ptr(), B, block_tables.data_ptr(),
+                                max_blocks, page, free_list.data_ptr(), n_blocks,
+                                free_count.data_ptr(), lens_out.data_ptr(),
+                                free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+                                n_slots, refused.data_ptr(), s)
+    if st:
+        _check("fq_page_step", st)
     return lens_out, cu_new, slots, refused
+
+
+def _kv4_dtype(t) -> int:
+    import torch
+    return FQ_BF16 if t.dtype is torch.bfloat16 else _dtype_code(t)
 
 
 def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=None):
@@ -495,27 +525,28 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     them at slots [n] (int32; tokens with a slot outside the pool are skipped) of the cache
     [n_blocks, Hkv, page / 16, unit bytes].  With values=True returns the quantised values
     (k_values, v_values) [n, Hkv, d] in the inputs' type."""
-    import torch
-    dev = _same_device(k, v, slots, cache)
+    dev = _device_index(k, v, slots, cache)
     if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v: two tensors [n, Hkv, d] of one type")
     n, hkv, d = k.shape
-    if n > 0 and (k.stride(2) != 1 or v.stride(2) != 1):
+    k0, k1, k2 = k.stride()
+    v0, v1, v2 = v.stride()
+    if n > 0 and (k2 != 1 or v2 != 1):
         raise ValueError("k and v: the last axis has to be contiguous")
     _int32("slots", slots, (n,))
     n_blocks, cache_hkv, page = _kv4_cache(cache, d, group)
     if cache_hkv != hkv:
         raise ValueError(f"cache of {cache_hkv} kv heads, keys of {hkv}")
-    dt = _kv4_dtype(k)
-    kv = vv = None
-    with _On(dev, stream) as s:
+    kv = vv = kp = vp = None
+    with _on(dev, stream) as s:
         if values:
-            kv = torch.empty((n, hkv, d), dtype=k.dtype, device=dev)
-            vv = torch.empty((n, hkv, d), dtype=k.dtype, device=dev)
-        st = lib().fq_kv4_write(_ptr(k), _ptr(v), dt, n, hkv, d, k.stride(0), k.stride(1),
-                                v.stride(0), v.stride(1), _ptr(slots), _ptr(cache), n_blocks, page,
-                                group, _ptr(kv), _ptr(vv), s)
-    _check("fq_kv4_write", st)
+            kv, vv = k.new_empty((2, n, hkv, d)).unbind(0)
+            kp, vp = kv.data_ptr(), vv.data_ptr()
+        st = lib().fq_kv4_write(k.data_ptr(), v.data_ptr(), _kv4_dtype(k), n, hkv, d, k0, k1, v0,
+                                v1, slots.data_ptr(), cache.data_ptr(), n_blocks, page, group, kp,
+                                vp, s)
+    if st:
+        _check("fq_kv4_write", st)
     return (kv, vv) if values else None
 
 
@@ -527,34 +558,39 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: i
     (int32).  cu_q [B + 1] (int32) gives the sequences' rows of q, at most max_q each; without it
     every sequence has one.  window > 0: only the last `window` tokens are seen.  Returns out
     [n_q, Hq, d] of q's type."""
-    import torch
-    dev = _same_device(q, cache, block_tables, kv_lens, cu_q, out, workspace)
-    if q.dim() != 3:
-        raise ValueError("q: [n_q, Hq, d]")
+    dev = _device_index(q, cache, block_tables, kv_lens, cu_q, out, workspace)
+    if q.dim() != 3 or block_tables.dim() != 2:
+        raise ValueError("q: [n_q, Hq, d]; block_tables: [B, max_blocks]")
     n_q, hq, d = q.shape
-    if n_q > 0 and q.stride(2) != 1:
+    q0, q1, q2 = q.stride()
+    if n_q > 0 and q2 != 1:
         raise ValueError("q: the last axis has to be contiguous")
     n_blocks, hkv, page = _kv4_cache(cache, d, group)
     B = kv_lens.numel()
+    max_blocks = block_tables.shape[1]
     _int32("kv_lens", kv_lens, (B,))
-    if block_tables.dim() != 2 or block_tables.shape[0] != B:
-        raise ValueError("block_tables: [B, max_blocks]")
-    _int32("block_tables", block_tables)
+    _int32("block_tables", block_tables, (B, max_blocks))
+    cu = None
     if cu_q is not None:
         _int32("cu_q", cu_q, (B + 1,))
-    dt = _kv4_dtype(q)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _On(dev, stream) as s:
+        cu = cu_q.data_ptr()
+    with _on(dev, stream) as s:
         if out is None:
-            out = torch.empty((n_q, hq, d), dtype=q.dtype, device=dev)
-        elif tuple(out.shape) != (n_q, hq, d) or out.dtype != q.dtype or not out.is_contiguous():
+            out = q.new_empty((n_q, hq, d))
+        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
             raise ValueError("out: a contiguous tensor of q's shape and type")
         if workspace is None:
-            workspace = torch.empty((fq_kv4_attn_workspace_bytes(d),), dtype=torch.uint8, device=dev)
-        st = lib().fq_kv4_attn(_ptr(q), dt, n_q, hq, d, q.stride(0), q.stride(1), _ptr(cu_q), B,
-                               max_q, _ptr(cache), n_blocks, hkv, page, group, _ptr(block_tables),
-                               block_tables.shape[1], _ptr(kv_lens), window, float(scale),
-                               _ptr(out), _ptr(workspace),
-                               workspace.numel() * workspace.element_size(), s)
-    _check("fq_kv4_attn", st)
+            ws_bytes = _KV4_WS.get(d)
+            if ws_bytes is None:
+                ws_bytes = _KV4_WS[d] = fq_kv4_attn_workspace_bytes(d)
+            workspace = cache.new_empty((ws_bytes,))
+        else:
+            ws_bytes = workspace.numel() * workspace.element_size()
+        st = lib().fq_kv4_attn(q.data_ptr(), _kv4_dtype(q), n_q, hq, d, q0, q1, cu, B, max_q,
+                               cache.data_ptr(), n_blocks, hkv, page, group,
+                               block_tables.data_ptr(), max_blocks, kv_lens.data_ptr(), window,
+                               1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
+                               workspace.data_ptr(), ws_bytes, s)
+    if st:
+        _check("fq_kv4_attn", st)
     return out

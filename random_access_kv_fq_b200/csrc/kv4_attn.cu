@@ -35,11 +35,14 @@ namespace {
 __device__ unsigned int g_kv4_wait_timeouts = 0;  // blocks whose bounded waits gave up
 
 constexpr int kCtas = 148;       // one block per SM
-constexpr int kStages = 4;       // units of a warp's ring
+constexpr int kChunk = 2;        // units of a stage of a warp's ring: one wait for 32 tokens
 constexpr int kItemTokens = 48;  // an item's fixed cost, in tokens (its queries and its end)
 
 template <int NT>
 constexpr int kWarpsOf = NT == 1 ? 16 : 12;
+// stages of a ring: ~10 KB a warp, 160 KB of an SM's copies in flight or in use
+template <int D>
+constexpr int kStagesOf = D == 64 ? 4 : 2;
 
 // What a block leaves for the second kernel: [kCtas][2] parts, part 0 of an item begun before the
 // block's range, part 1 of an item begun in it that goes on behind it.
@@ -87,7 +90,12 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   return s;
 }
 
-__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t b, uint32_t c) { return (a & b) | c; }
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
 
 __device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
 __device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
@@ -100,12 +108,21 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void mma8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+// the same, and the k = 8 form, with nothing to add to
+__device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
   asm volatile(
       "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-      "{%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(b0));
+      "{%7,%7,%7,%7};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
@@ -280,23 +297,18 @@ struct Warp {
     }
     float x[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
-#pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
       float acc[NT][4];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
 #pragma unroll
       for (int kb = gr * G / 32; kb < (gr + 1) * G / 32; ++kb) {
         const uint32_t lowm = 0x000F000Fu, highm = 0x00F000F0u;
         const uint32_t a = k0[kb] >> 8, b = k1[kb] >> 8;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          mma16(acc[nt], k0[kb] & lowm, k1[kb] & lowm, k0[kb] & highm, k1[kb] & highm, q[nt][kb][0], q[nt][kb][1]);
+          if (kb == gr * G / 32)
+            mma16_first(acc[nt], k0[kb] & lowm, k1[kb] & lowm, k0[kb] & highm, k1[kb] & highm, q[nt][kb][0], q[nt][kb][1]);
+          else
+            mma16(acc[nt], k0[kb] & lowm, k1[kb] & lowm, k0[kb] & highm, k1[kb] & highm, q[nt][kb][0], q[nt][kb][1]);
           mma16(acc[nt], a & lowm, b & lowm, a & highm, b & highm, q[nt][kb][2], q[nt][kb][3]);
         }
       }
@@ -304,27 +316,28 @@ struct Warp {
       const float f0 = gr % 2 ? __high2float(p0) : __low2float(p0);
       const float f1 = gr % 2 ? __high2float(p1) : __low2float(p1);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        x[nt][0] = fmaf(acc[nt][0], f0, x[nt][0]);
-        x[nt][1] = fmaf(acc[nt][1], f0, x[nt][1]);
-        x[nt][2] = fmaf(acc[nt][2], f1, x[nt][2]);
-        x[nt][3] = fmaf(acc[nt][3], f1, x[nt][3]);
-      }
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          x[nt][i] = gr == 0 ? acc[nt][i] * (i < 2 ? f0 : f1) : fmaf(acc[nt][i], i < 2 ? f0 : f1, x[nt][i]);
     }
+    // x: scores over kappa; y: base-2 logarithms of the weights
+    float y[NT][4];
     bool passes = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      mma8(acc, z0, z1, qz[nt][0]);
+      float acc[4];
+      mma8_first(acc, z0, z1, qz[nt][0]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[nt][i] = fmaf(x[nt][i], 16777216.f, acc[i]) * kappa[nt][i & 1];
+        x[nt][i] = fmaf(x[nt][i], 16777216.f, acc[i]);
+        y[nt][i] = fmaf(x[nt][i], kappa[nt][i & 1], -m[nt][i & 1]);
         if (MASK) {
           // rows of the product are tokens (g >> 1) + 4 (g & 1), and 8 further
           const int pos = pos0 + (g >> 1) + 4 * (g & 1) + 4 * (i & 2);
-          if (pos >= hi[nt][i & 1] || pos < lo[nt][i & 1]) x[nt][i] = -INFINITY;
+          if (pos >= hi[nt][i & 1] || pos < lo[nt][i & 1]) y[nt][i] = -INFINITY;
         }
-        passes |= x[nt][i] > m[nt][i & 1] + 8.f;
+        passes |= y[nt][i] > 8.f;
       }
     }
     if (__any_sync(~0u, passes)) {
@@ -332,11 +345,15 @@ struct Warp {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = fmaxf(x[nt][c], x[nt][c + 2]);
+          const float xa = y[nt][c] == -INFINITY ? -INFINITY : x[nt][c] * kappa[nt][c];
+          const float xb = y[nt][c + 2] == -INFINITY ? -INFINITY : x[nt][c + 2] * kappa[nt][c];
+          float top = fmaxf(xa, xb);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
           top = fmaxf(top, m[nt][c]);
           const float f = ex2(m[nt][c] - top);
+          y[nt][c] = xa - top;
+          y[nt][c + 2] = xb - top;
           m[nt][c] = top;
           l[nt][c] *= f;
 #pragma unroll
@@ -350,7 +367,7 @@ struct Warp {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[nt][i] = ex2(x[nt][i] - m[nt][i & 1]);
+      for (int i = 0; i < 4; ++i) x[nt][i] = ex2(y[nt][i]);
       l[nt][0] += x[nt][0] + x[nt][2];
       l[nt][1] += x[nt][1] + x[nt][3];
 #pragma unroll
@@ -481,8 +498,8 @@ template <typename T, int D, int G, int NT>
 __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift) {
   using W_ = Warp<T, D, G, NT>;
   using P = Part<NT, D>;
-  constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB;
-  constexpr size_t kSlot = kStages * UB > (int)sizeof(P) ? kStages * UB : sizeof(P);
+  constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
+  constexpr size_t kRing = kStages * kChunk * UB, kSlot = kRing > sizeof(P) ? kRing : sizeof(P);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* rings = smem;                                          // [W][kSlot]
   P* heads = reinterpret_cast<P*>(smem + W * kSlot);              // [W]
@@ -494,7 +511,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   const int r = a.hq / a.hkv;
 
   if (tid == 0) gave_up = 0;
-  if (lane < kStages) ptx::mbar_init(&bars[warp][lane], 1);
+  if (lane < kStages) ptx::mbar_init(&bars[warp][lane], kChunk);
   if (lane < 2) hdr[warp][lane].state = 0;
   ptx::fence_mbar_init();
 
@@ -547,8 +564,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   W_ st;
   uint8_t* ring = rings + warp * kSlot;
   const uint32_t ring32 = ptx::smem_u32(ring);
-  int stage = 0;
-  uint32_t phase = 0;
+  uint32_t count = 0;  // chunks so far: the ring's stage and its barrier's parity
   bool ok = true;
   int64_t at = x0;
   while (at < x1 && ok) {
@@ -581,57 +597,65 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
 
     st.reset();
     if (u0 < u1) {
-      // Copies run kStages units ahead; lane i issues units i, i + 32, ... of the range, from the
-      // table entry that it holds.  A unit on a page outside the pool is neither copied nor used.
+      // Copies run up to kStages chunks ahead.  Lane i issues units i, i + 32, ... of the range, from
+      // the table entry that it holds; a unit behind the range or on a page outside the pool only
+      // counts as arrived, and `gone` has its bit.
       const int32_t* table = a.tables + (int64_t)b * a.max_blocks;
-      const int unit_mask = (1 << (page_shift - 4)) - 1;
-      auto entry = [&](int i) {
-        const int u = base_u + i;
-        return i < u1 ? __ldg(table + (u >> (page_shift - 4))) : -1;
-      };
-      int id = entry(u0 + lane), id_next = entry(u0 + 32 + lane);
-      uint32_t there = 0;  // of the last 32 units that were issued (bit: unit mod 32)
-      int put_stage = stage;
-      auto issue = [&](int i) {
-        const int who = (i - u0) & 31;
-        if (who == 0 && i != u0) {
-          id = id_next;
-          id_next = entry(i + 32 + lane);
+      const int n_units = u1 - u0, chunks = (n_units + kChunk - 1) / kChunk;
+      const int shift = page_shift - 4;
+      auto entry = [&](int i) { return i < n_units ? __ldg(table + ((base_u + u0 + i) >> shift)) : -1; };
+      const uint8_t* src = nullptr;
+      int id_next = entry(lane);
+      uint32_t gone = 0, gone_next = 0;  // of the 32 units that are being used, and being issued
+      auto issue = [&](int j) {
+        const int who = (j * kChunk) & 31;
+        if (who == 0) {
+          const int id = id_next, i = j * kChunk + lane;
+          id_next = entry(i + 32);
+          src = nullptr;
+          if (id >= 0 && id < a.n_blocks)
+            src = a.cache + ((((int64_t)id * a.hkv + head) << shift) + ((base_u + u0 + i) & ((1 << shift) - 1))) * UB;
+          gone_next = __ballot_sync(~0u, src == nullptr);
         }
-        const bool good = id >= 0 && id < a.n_blocks;
-        const uint32_t all = __ballot_sync(~0u, good);
-        const bool has = (all >> who) & 1;
-        there = (there & ~(1u << who)) | ((uint32_t)has << who);
-        if (has) {
-          if (lane == who) {
-            const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + head) << (page_shift - 4)) + ((base_u + i) & unit_mask)) * UB;
-            ptx::mbar_arrive_expect_tx(&bars[warp][put_stage], UB);
-            ptx::bulk_load(ring + put_stage * UB, src, UB, &bars[warp][put_stage]);
+        if ((unsigned)(lane - who) < kChunk) {
+          const uint32_t at_stage = (count + j) % kStages;
+          uint64_t* bar = &bars[warp][at_stage];
+          if (src) {
+            ptx::mbar_arrive_expect_tx(bar, UB);
+            ptx::bulk_load(ring + (at_stage * kChunk + lane - who) * UB, src, UB, bar);
+          } else {
+            ptx::mbar_arrive(bar);
           }
-          put_stage = put_stage + 1 == kStages ? 0 : put_stage + 1;
         }
       };
-      // units issued and not used are at most kStages
-      int put = u0;
-      for (; put < u1 && put < u0 + kStages; ++put) issue(put);
+      for (int j = 0; j < chunks && j < kStages; ++j) issue(j);
       st.load_queries(a, s, head, rb, r, lane);
       const int all_end = past + row0 / r, all_first = a.window > 0 ? past + row1 / r - a.window : 0;
       // a wait that gives up ends the loop once the copies in flight had their time to land
-      for (int i = u0; i < u1 && (ok || i < put); ++i) {
-        if ((there >> ((i - u0) & 31)) & 1) {
-          ok = __all_sync(~0u, ptx::mbar_wait(&bars[warp][stage], (phase >> stage) & 1)) && ok;
-          phase ^= 1u << stage;
-          if (ok) {
-            const int pos0 = (base_u + i) * kUnit;
-            const uint32_t u = ring32 + stage * UB;
+      int landing = chunks;
+      for (int j = 0; j < landing; ++j) {
+        if (((j * kChunk) & 31) == 0) gone = gone_next;
+        const uint32_t at_stage = (count + j) % kStages, parity = (count + j) / kStages & 1;
+        if (!__all_sync(~0u, ptx::mbar_try(&bars[warp][at_stage], parity)) &&
+            !__all_sync(~0u, ptx::mbar_wait(&bars[warp][at_stage], parity)) && ok) {
+          ok = false;
+          landing = min(chunks, j + kStages);
+        }
+        if (ok) {
+          const uint32_t skip = gone >> ((j * kChunk) & 31);
+          int pos0 = (base_u + u0 + j * kChunk) * kUnit;
+          uint32_t u = ring32 + at_stage * kChunk * UB;
+#pragma unroll 1
+          for (int i = 0; i < kChunk; ++i, pos0 += kUnit, u += UB) {
+            if ((skip >> i) & 1) continue;
             if (pos0 >= all_first && pos0 + kUnit <= all_end) st.template unit<false>(u, pos0, first, end, lane);
             else st.template unit<true>(u, pos0, first, end, lane);
           }
-          stage = stage + 1 == kStages ? 0 : stage + 1;
           __syncwarp();
+          if (j + kStages < chunks) issue(j + kStages);
         }
-        if (put < u1 && ok) issue(put++);
       }
+      count += chunks;
       st.finish_sums();
     }
     if (from == 0 && to == cost) {
@@ -756,8 +780,8 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
 template <typename T, int D, int G, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   using P = Part<NT, D>;
-  constexpr int W = kWarpsOf<NT>, UB = unit_bytes(D, G);
-  constexpr size_t slot = kStages * UB > (int)sizeof(P) ? kStages * UB : sizeof(P);
+  constexpr int W = kWarpsOf<NT>;
+  constexpr size_t ring = kStagesOf<D> * kChunk * unit_bytes(D, G), slot = ring > sizeof(P) ? ring : sizeof(P);
   constexpr size_t rings = W * (slot + sizeof(P)), table = sizeof(int64_t) * kMaxRequests;
   constexpr size_t bytes = rings > table ? rings : table;
   static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
