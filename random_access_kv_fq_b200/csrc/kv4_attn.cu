@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<ui
 
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
@@ -111,14 +111,14 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
 // the same, and the k = 8 form, with nothing to add to
 __device__ __forceinline__ void mma16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
       "{%10,%10,%10,%10};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma8_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
       "{%7,%7,%7,%7};"
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -272,29 +272,34 @@ struct Warp {
       }
   }
 
-  // One unit at shared address `u`, whose first token is at position pos0.  MASK: some row does not
-  // see all of it; [first, end) is what any row sees.
-  template <bool MASK>
-  __device__ __forceinline__ void unit(uint32_t u, int pos0, int first, int end, int lane) {
+  // Where in a unit this lane reads: its key codes, key steps, value codes, value steps.
+  struct Place {
+    uint32_t k, ks, v, vs;
+  };
+  static __device__ __forceinline__ Place place(uint32_t u, int lane) {
     const int g = lane >> 2, t = lane & 3;
+    Place p{u + lane * (D / 8), u + off_ks(D) + g * 4 * NG,
+            u + off_v(D) + t * (D / 2) + (D == 128 ? ((2 * g) ^ ((t & 2) << 2)) * 4 : 4 * g),
+            u + off_vs(D, G) + t * 4 * NG + (g * (D / 8) / G) * 4};
+    // kept in registers: made again for every unit they would cost a twelfth of its instructions
+    asm volatile("" : "+r"(p.k), "+r"(p.ks), "+r"(p.v), "+r"(p.vs));
+    return p;
+  }
+
+  // One unit at `u`, whose first token is at position pos0.  MASK: some row may not see all of it;
+  // [first, end) is what any row sees.
+  template <bool MASK>
+  __device__ __forceinline__ void unit(const Place& u, int pos0, int first, int end, int lane) {
     uint32_t k0[KB], k1[KB];
-    lds<D / 8>(u + lane * (D / 8), k0);
-    lds<D / 8>(u + lane * (D / 8) + 4 * D, k1);
-    // steps of token rows g and g + 8, and the zero words that this lane feeds to the product
-    uint32_t s0[(NG + 1) / 2], s1[(NG + 1) / 2], z0, z1;
-    const uint32_t ks = u + off_ks(D) + g * 4 * NG;
-    if constexpr (NG == 1) {
-      lds<4>(ks, s0);
-      lds<4>(ks + 32, s1);
-      z0 = s0[0];
-      z1 = s1[0];
-    } else {
-      lds<2 * NG>(ks, s0);
-      lds<2 * NG>(ks + 32 * NG, s1);
-      const uint32_t zw = ks + 2 * NG + 4 * (t & (NG / 2 - 1));
-      lds<4>(zw, &z0);
-      lds<4>(zw + 32 * NG, &z1);
-    }
+    lds<D / 8>(u.k, k0);
+    lds<D / 8>(u.k + 4 * D, k1);
+    // steps and zeros of token rows g and g + 8: 2 NG numbers each, of which lane t feeds the product
+    // with the zeros of groups 2 (t & 1) and 2 (t & 1) + 1
+    uint32_t s0[NG], s1[NG];
+    lds<4 * NG>(u.ks, s0);
+    lds<4 * NG>(u.ks + 32 * NG, s1);
+    const uint32_t z0 = NG == 4 ? (lane & 1 ? s0[NG - 1] : s0[NG / 2]) : s0[NG - 1];
+    const uint32_t z1 = NG == 4 ? (lane & 1 ? s1[NG - 1] : s1[NG / 2]) : s1[NG - 1];
     float x[NT][4];
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
@@ -323,7 +328,7 @@ struct Warp {
     }
     // x: scores over kappa; y: base-2 logarithms of the weights
     float y[NT][4];
-    bool passes = false;
+    float high = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float acc[4];
@@ -334,13 +339,13 @@ struct Warp {
         y[nt][i] = fmaf(x[nt][i], kappa[nt][i & 1], -m[nt][i & 1]);
         if (MASK) {
           // rows of the product are tokens (g >> 1) + 4 (g & 1), and 8 further
-          const int pos = pos0 + (g >> 1) + 4 * (g & 1) + 4 * (i & 2);
+          const int pos = pos0 + (lane >> 3) + (lane & 4) + 4 * (i & 2);
           if (pos >= hi[nt][i & 1] || pos < lo[nt][i & 1]) y[nt][i] = -INFINITY;
         }
-        passes |= y[nt][i] > 8.f;
+        high = fmaxf(high, y[nt][i]);
       }
     }
-    if (__any_sync(~0u, passes)) {
+    if (__any_sync(~0u, high > 8.f)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -382,14 +387,12 @@ struct Warp {
     }
     // values: this lane's tokens are t + 4 i, its coordinates g D/8 .. + D/8 (all of one group)
     uint32_t w[4][D / 64], sz[4];
-    const uint32_t vb = u + off_v(D) + (D == 128 ? ((2 * g) ^ ((t & 2) << 2)) * 4 : 4 * g);
-    const uint32_t vs = u + off_vs(D, G) + t * 4 * NG + (g * (D / 8) / G) * 4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      lds<D / 16>(vb + (t + 4 * i) * (D / 2), w[i]);
-      lds<4>(vs + 16 * i * NG, &sz[i]);
+      lds<D / 16>(u.v + 4 * i * (D / 2), w[i]);
+      lds<4>(u.vs + 16 * i * NG, &sz[i]);
       if (MASK) {
-        const int pos = pos0 + t + 4 * i;
+        const int pos = pos0 + (lane & 3) + 4 * i;
         if (pos < first || pos >= end) sz[i] = 0;  // a token that nobody sees: its value becomes 0
       }
     }
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
 
   W_ st;
   uint8_t* ring = rings + warp * kSlot;
-  const uint32_t ring32 = ptx::smem_u32(ring);
+  const typename W_::Place place = W_::place(ptx::smem_u32(ring), lane);
   uint32_t count = 0;  // chunks so far: the ring's stage and its barrier's parity
   bool ok = true;
   int64_t at = x0;
@@ -642,14 +645,27 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
           landing = min(chunks, j + kStages);
         }
         if (ok) {
-          const uint32_t skip = gone >> ((j * kChunk) & 31);
-          int pos0 = (base_u + u0 + j * kChunk) * kUnit;
-          uint32_t u = ring32 + at_stage * kChunk * UB;
+          const uint32_t skip = gone >> ((j * kChunk) & 31) & ((1u << kChunk) - 1);
+          const int pos0 = (base_u + u0 + j * kChunk) * kUnit;
+          typename W_::Place u = place;
+          const uint32_t off = at_stage * kChunk * UB;
+          u.k += off;
+          u.ks += off;
+          u.v += off;
+          u.vs += off;
+          if (pos0 >= all_first && pos0 + kChunk * kUnit <= all_end && skip == 0) {
+#pragma unroll
+            for (int i = 0; i < kChunk; ++i)
+              st.template unit<false>(typename W_::Place{u.k + i * UB, u.ks + i * UB, u.v + i * UB, u.vs + i * UB}, 0, 0, 0, lane);
+          } else {
 #pragma unroll 1
-          for (int i = 0; i < kChunk; ++i, pos0 += kUnit, u += UB) {
-            if ((skip >> i) & 1) continue;
-            if (pos0 >= all_first && pos0 + kUnit <= all_end) st.template unit<false>(u, pos0, first, end, lane);
-            else st.template unit<true>(u, pos0, first, end, lane);
+            for (int i = 0; i < kChunk; ++i) {
+              if (!((skip >> i) & 1)) st.template unit<true>(u, pos0 + i * kUnit, first, end, lane);
+              u.k += UB;
+              u.ks += UB;
+              u.v += UB;
+              u.vs += UB;
+            }
           }
           __syncwarp();
           if (j + kStages < chunks) issue(j + kStages);
