@@ -47,8 +47,8 @@ constexpr int kStagesOf = D == 64 ? 4 : 2;
 // What a block leaves for the second kernel: [kCtas][2] parts, part 0 of an item begun before the
 // block's range, part 1 of an item begun in it that goes on behind it.
 struct PartHeader {
-  int state;  // 0: none, 1: goes on, 3: the item's last part
-  int b, head, rb;
+  int state;             // 0: none, 1: goes on, 3: the item's last part
+  int q0, rows, head, rb;  // where its rows are
 };
 template <int NT, int D>
 struct Part {
@@ -62,6 +62,7 @@ struct Seq {
   int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
   int64_t k0;                  // cost of row block rb: k0 + slope (rb + 1), in 1 / (hq / hkv) tokens
   int slope;
+  __device__ int64_t cost(int rb) const { return k0 + (int64_t)slope * (rb + 1); }
   __device__ int64_t upto(int rb) const { return rb * k0 + (int64_t)slope * rb * (rb + 1) / 2; }
 };
 
@@ -185,36 +186,53 @@ struct Warp {
     }
   }
 
-  // Queries of row block rb of (sequence, kv head): row r is query token r / R, head r % R.
-  __device__ __forceinline__ void load_queries(const AttnArgs& a, const Seq& s, int head, int rb, int r, int lane) {
+  // Queries of row block rb of (sequence, kv head): row r is query token r / R, head r % R.  Asked
+  // for before the first unit is, used while it is on its way.
+  __device__ __forceinline__ void fetch_queries(const AttnArgs& a, const Seq& s, int head, int rb, uint32_t r, int lane) {
     const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const uint32_t row = rb * 8 * NT + nt * 8 + g;
+      const bool in = row < (uint32_t)s.rows;
+      const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(s.q0 + tok) * a.q_tok +
+                            (int64_t)(head * r + hh) * a.q_head + 8 * t;
+      const bool wide = in && reinterpret_cast<uintptr_t>(src) % 16 == 0;
+#pragma unroll
+      for (int kb = 0; kb < KB; ++kb) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (wide) {
+          w = __ldg(reinterpret_cast<const uint4*>(src + 32 * kb));
+        } else if (in) {
+          const uint16_t* p = src + 32 * kb;
+          w.x = __ldg(p) | (uint32_t)__ldg(p + 1) << 16;
+          w.y = __ldg(p + 2) | (uint32_t)__ldg(p + 3) << 16;
+          w.z = __ldg(p + 4) | (uint32_t)__ldg(p + 5) << 16;
+          w.w = __ldg(p + 6) | (uint32_t)__ldg(p + 7) << 16;
+        }
+        q[nt][kb][0] = w.x;
+        q[nt][kb][1] = w.y;
+        q[nt][kb][2] = w.z;
+        q[nt][kb][3] = w.w;
+      }
+    }
+  }
+
+  __device__ __forceinline__ void convert_queries(const AttnArgs& a, const Seq& s, int rb, uint32_t r, int lane) {
+    const int t = lane & 3;
     const int past = s.n - s.m + 1;
     float kap[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int row = rb * 8 * NT + nt * 8 + g;
-      const bool in = row < s.rows;
-      const int tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(s.q0 + tok) * a.q_tok +
-                            (int64_t)(head * r + hh) * a.q_head + 8 * t;
-      const bool wide = in && reinterpret_cast<uintptr_t>(src) % 16 == 0;
       float x[KB][8];
       float top = 0.f;
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) {
-        uint16_t w[8];
-        if (wide) {
-          *reinterpret_cast<uint4*>(w) = __ldg(reinterpret_cast<const uint4*>(src + 32 * kb));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = in ? __ldg(src + 32 * kb + e) : 0;
-        }
+      for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          x[kb][e] = q_float<T>(w[e]);
+          x[kb][e] = q_float<T>((uint16_t)(q[nt][kb][e / 2] >> (16 * (e & 1))));
           top = fmaxf(top, fabsf(x[kb][e]));
         }
-      }
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
       top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
       // the row times 2^-e lies within +-2^8: exact in fp16 but for what is 2^-28 of the largest
@@ -266,8 +284,8 @@ struct Warp {
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         kappa[nt][c] = __shfl_sync(~0u, kap[nt], 8 * t + 4 * c);
-        const int row = min(rb * 8 * NT + nt * 8 + 2 * t + c, s.rows - 1);
-        hi[nt][c] = past + row / r;
+        const uint32_t row = min(rb * 8 * NT + nt * 8 + 2 * t + c, s.rows - 1);
+        hi[nt][c] = past + (int)(row / r);
         lo[nt][c] = a.window > 0 ? hi[nt][c] - a.window : 0;
       }
   }
@@ -456,15 +474,15 @@ struct Warp {
     }
   }
 
-  __device__ __forceinline__ void write_out(const AttnArgs& a, const Seq& s, int head, int rb, int r, int lane) const {
+  __device__ __forceinline__ void write_out(const AttnArgs& a, const Seq& s, int head, int rb, uint32_t r, int lane) const {
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int row = rb * 8 * NT + nt * 8 + 2 * t + c;
-        if (row >= s.rows) continue;
-        const int tok = row / r;
+        const uint32_t row = rb * 8 * NT + nt * 8 + 2 * t + c;
+        if (row >= (uint32_t)s.rows) continue;
+        const uint32_t tok = row / r;
         const float inv = l[nt][c] > 0.f ? 1.0f / l[nt][c] : 0.f;
         T* dst = static_cast<T*>(a.out) + ((int64_t)(s.q0 + tok) * a.hq + head * r + row - tok * r) * D + g * (D / 8);
 #pragma unroll
@@ -480,25 +498,49 @@ struct Warp {
   }
 };
 
-// Merged accumulators of one fragment word of an item into out: rows 2 t and 2 t + 1, two coordinates.
+// One fragment word of an item's merged accumulators into out: rows 2 t and 2 t + 1, two coordinates.
 template <typename T, int D, int NT>
-__device__ __forceinline__ void write_merged(const AttnArgs& a, int b, int head, int rb, int e, float4 o, float l0, float l1) {
+__device__ __forceinline__ void write_merged(const AttnArgs& a, const PartHeader& h, int e, float4 o, float l0, float l1) {
   const int lane = e & 31, mt = (e >> 5) % (D / 16), nt = (e >> 5) / (D / 16), g = lane >> 2, t = lane & 3;
-  const int r = a.hq / a.hkv;
-  const Seq s = load_seq<8 * NT>(a, b, r);
+  const uint32_t r = a.hq / a.hkv;
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const int row = rb * 8 * NT + nt * 8 + 2 * t + c;
-    if (row >= s.rows) continue;
-    const int tok = row / r;
+    const uint32_t row = h.rb * 8 * NT + nt * 8 + 2 * t + c;
+    if (row >= (uint32_t)h.rows) continue;
+    const uint32_t tok = row / r;
     const float l = c ? l1 : l0, inv = l > 0.f ? 1.0f / l : 0.f;
-    T* dst = static_cast<T*>(a.out) + ((int64_t)(s.q0 + tok) * a.hq + head * r + row - tok * r) * D + g * (D / 8) + 2 * mt;
+    T* dst = static_cast<T*>(a.out) + ((int64_t)(h.q0 + tok) * a.hq + h.head * r + row - tok * r) * D + g * (D / 8) + 2 * mt;
     *reinterpret_cast<uint32_t*>(dst) = pack_out<T>((c ? o.y : o.x) * inv, (c ? o.w : o.z) * inv);
   }
 }
 
+// Running join of an item's parts, for one fragment word: rows 0 and 1 of its four numbers.
+struct Join {
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
+  __device__ __forceinline__ void add(float4 y, float2 m, float2 l) {
+    const float n0 = fmaxf(m0, m.x), n1 = fmaxf(m1, m.y);
+    const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1), b0 = ex2(m.x - n0), b1 = ex2(m.y - n1);
+    o.x = fmaf(y.x, b0, o.x * a0);
+    o.y = fmaf(y.y, b1, o.y * a1);
+    o.z = fmaf(y.z, b0, o.z * a0);
+    o.w = fmaf(y.w, b1, o.w * a1);
+    l0 = fmaf(l.x, b0, l0 * a0);
+    l1 = fmaf(l.y, b1, l1 * a1);
+    m0 = n0;
+    m1 = n1;
+  }
+};
+
+// floor(x / d) for 0 <= x < 2^52, given 1 / d
+__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d, double inv) {
+  int64_t q = (int64_t)((double)x * inv);
+  const int64_t rest = x - q * d;
+  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
+}
+
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift, double inv_step) {
   using W_ = Warp<T, D, G, NT>;
   using P = Part<NT, D>;
   constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
@@ -508,7 +550,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   P* heads = reinterpret_cast<P*>(smem + W * kSlot);              // [W]
   __shared__ uint64_t bars[W][kStages];
   __shared__ PartHeader hdr[W][2];
-  __shared__ int64_t scan[W];
+  __shared__ int64_t scan[W], start_base[W];
+  __shared__ int start_b[W];
+  __shared__ int4 groups[2 * W];
   __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = a.hq / a.hkv;
@@ -518,17 +562,13 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   if (lane < 2) hdr[warp][lane].state = 0;
   ptx::fence_mbar_init();
 
-  // sums of the sequences' costs, in shared memory (where the rings will be)
-  int64_t* sums = reinterpret_cast<int64_t*>(smem);
-  const int per = (a.B + 32 * W - 1) / (32 * W);
+  // The line of all items' costs: each thread adds up its sequences', and the one whose cost holds
+  // the start of a warp's range tells that warp.
+  const int per = (a.B + 32 * W - 1) / (32 * W), b_mine = tid * per;
   int64_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int b = tid * per + i;
-    if (b < a.B) {
-      const Seq s = load_seq<NB>(a, b, r);
-      mine += a.hkv * s.upto(s.blocks);
-      sums[b] = mine;
-    }
+  for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
+    const Seq s = load_seq<NB>(a, b, r);
+    mine += a.hkv * s.upto(s.blocks);
   }
   int64_t x = mine;
 #pragma unroll
@@ -539,28 +579,30 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   if (lane == 31) scan[warp] = x;
   __syncthreads();
   int64_t below = x - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < W; ++w) {
     if (w < warp) below += scan[w];
     total += scan[w];
   }
-  for (int i = 0; i < per; ++i)
-    if (tid * per + i < a.B) sums[tid * per + i] += below;
-  ptx::fence_proxy_async_smem();  // copies will write where the sums are
-  __syncthreads();
-
-  // this warp's range of the line, at least a unit long
+  // a range is at least a unit long
   const int64_t span = max((total + kCtas * W - 1) / (kCtas * W), (int64_t)kUnit * r);
-  const int64_t x0 = (int64_t)(blockIdx.x * W + warp) * span, x1 = min(total, x0 + span);
-  int b = 0;
-  int64_t base = 0;
-  if (x0 < x1) {
-    int lo = 0, hi = a.B - 1;  // the first sequence whose sum is past x0
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (sums[mid] > x0) hi = mid; else lo = mid + 1;
+  const int64_t block0 = (int64_t)blockIdx.x * W * span;
+  if (below + mine > block0 && below < block0 + W * span) {
+    for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
+      int64_t cost = mine;
+      if (per > 1) {
+        const Seq s = load_seq<NB>(a, b, r);
+        cost = a.hkv * s.upto(s.blocks);
+      }
+      for (int w = 0; w < W; ++w) {
+        const int64_t x0 = block0 + w * span;
+        if (x0 >= below && x0 < below + cost) {
+          start_b[w] = b;
+          start_base[w] = below;
+        }
+      }
+      below += cost;
     }
-    b = lo;
-    base = b > 0 ? sums[b - 1] : 0;
   }
   __syncthreads();
 
@@ -569,34 +611,37 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   const typename W_::Place place = W_::place(ptx::smem_u32(ring), lane);
   uint32_t count = 0;  // chunks so far: the ring's stage and its barrier's parity
   bool ok = true;
-  int64_t at = x0;
-  while (at < x1 && ok) {
-    // the item at `at`
-    const Seq s = load_seq<NB>(a, b, r);
-    const int64_t one = s.upto(s.blocks), in_seq = at - base;
-    if (in_seq >= a.hkv * one) {
-      base += a.hkv * one;
-      ++b;
-      continue;
-    }
-    const int head = (int)(in_seq / one);
+  const int64_t x0 = block0 + warp * span, x1 = min(total, x0 + span);
+  int64_t item0 = x0, from = 0;
+  int b = 0, head = 0, rb = 0;
+  Seq s = {};
+  if (x0 < x1) {
+    // the item at x0
+    b = start_b[warp];
+    s = load_seq<NB>(a, b, r);
+    const int64_t one = s.upto(s.blocks), in_seq = x0 - start_base[warp];
+    head = (int)quotient(in_seq, one, 1.0 / (double)one);
     const int64_t in_head = in_seq - head * one;
-    int rb = 0, above = s.blocks;
+    int above = s.blocks;
     while (above - rb > 1) {
       const int mid = (rb + above) >> 1;
       if (s.upto(mid) <= in_head) rb = mid; else above = mid;
     }
-    const int64_t item0 = base + head * one + s.upto(rb), cost = s.upto(rb + 1) - s.upto(rb);
-    const int64_t from = at - item0, to = min(x1 - item0, cost);
-    at = item0 + to;
+    from = in_head - s.upto(rb);
+    item0 = x0 - from;
+  }
+  for (; item0 + from < x1 && ok;) {
+    const int64_t cost = s.cost(rb), to = min(x1 - item0, cost);
     // tokens that any row of the block sees, in units; the part of them in this range
-    const int past = s.n - s.m + 1, row0 = rb * NB, row1 = min(row0 + NB, s.rows) - 1;
-    const int end = max(0, past + row1 / r);
-    const int first = a.window > 0 ? max(0, past + row0 / r - a.window) : 0;
+    const int past = s.n - s.m + 1;
+    const uint32_t row0 = rb * NB, row1 = min(rb * NB + NB, s.rows) - 1;
+    const int tok0 = row0 / (uint32_t)r, tok1 = row1 / (uint32_t)r;
+    const int end = max(0, past + tok1);
+    const int first = a.window > 0 ? max(0, past + tok0 - a.window) : 0;
     const int base_u = first / kUnit, units = end > first ? (end + kUnit - 1) / kUnit - base_u : 0;
     const int64_t fixed = (int64_t)kItemTokens * r, step = (int64_t)kUnit * r;
-    const int u0 = from <= fixed ? 0 : (int)min((int64_t)units, (from - fixed + step - 1) / step);
-    const int u1 = to == cost ? units : to <= fixed ? 0 : (int)min((int64_t)units, (to - fixed + step - 1) / step);
+    const int u0 = from <= fixed ? 0 : (int)min((int64_t)units, quotient(from - fixed + step - 1, step, inv_step));
+    const int u1 = to == cost ? units : to <= fixed ? 0 : (int)min((int64_t)units, quotient(to - fixed + step - 1, step, inv_step));
 
     st.reset();
     if (u0 < u1) {
@@ -631,9 +676,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
           }
         }
       };
+      st.fetch_queries(a, s, head, rb, r, lane);
       for (int j = 0; j < chunks && j < kStages; ++j) issue(j);
-      st.load_queries(a, s, head, rb, r, lane);
-      const int all_end = past + row0 / r, all_first = a.window > 0 ? past + row1 / r - a.window : 0;
+      st.convert_queries(a, s, rb, r, lane);
+      const int all_end = past + tok0, all_first = a.window > 0 ? past + tok1 - a.window : 0;
       // a wait that gives up ends the loop once the copies in flight had their time to land
       int landing = chunks;
       for (int j = 0; j < landing; ++j) {
@@ -680,116 +726,115 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
       // an item begun before this range leaves its part beside the ring, one that goes on in it
       const int k = from > 0 ? 0 : 1;
       st.write_part(k == 0 ? heads + warp : reinterpret_cast<P*>(ring), lane);
-      if (lane == 0) hdr[warp][k] = PartHeader{to == cost ? 3 : 1, b, head, rb};
+      if (lane == 0) hdr[warp][k] = PartHeader{to == cost ? 3 : 1, s.q0, s.rows, head, rb};
+    }
+    // the next item of the line
+    item0 += cost;
+    from = 0;
+    if (++rb == s.blocks) {
+      rb = 0;
+      if (++head == a.hkv) {
+        head = 0;
+        if (item0 < x1) do s = load_seq<NB>(a, ++b, r); while (s.blocks == 0);
+      }
     }
   }
   if (!ok) gave_up = 1;
+  asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   if (tid == 0 && gave_up) atomicAdd(&g_kv4_wait_timeouts, 1u);
 
-  // Join the parts of each item, in order; what begins before or ends behind the block goes to the
-  // workspace.
+  // Join the parts of each item; what begins before or ends behind the block goes to the workspace.
+  // Slot 2 w + k holds part k of warp w.  An item's parts are a part 1 (or, if begun before the
+  // block, warp 0's part 0) and the next warps' parts 0 up to its last one.
   PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
   P* out_part = reinterpret_cast<P*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
-  bool left[2] = {false, false};
-  auto part_of = [&](int i) -> const P& {
-    return (i & 1) ? *reinterpret_cast<const P*>(rings + (i >> 1) * kSlot) : heads[i >> 1];
-  };
-  for (int i = 0; i < 2 * W;) {
-    const PartHeader h = hdr[i >> 1][i & 1];
-    if (h.state == 0) { ++i; continue; }
-    // parts i, then the next warps' parts 0, until the item's last one
-    int count = 1, last = h.state;
-    const bool begun = i & 1;
-    for (int j = (i >> 1) + 1; last == 1 && j < W && hdr[j][0].state != 0; ++j) {
-      last = hdr[j][0].state;
-      ++count;
+  const int state = lane < 2 * W ? hdr[lane >> 1][lane & 1].state : 0;
+  const uint32_t has = __ballot_sync(~0u, state != 0), ends = __ballot_sync(~0u, state == 3) & 0x55555555u;
+  const bool begins = state != 0 && ((lane & 1) || lane == 0);
+  const uint32_t starts = __ballot_sync(~0u, begins);
+  if (warp == 0) {
+    // the next warps' parts 0, up to one that ends the item or is missing
+    const int next = (lane | 1) + 1;
+    const uint32_t stop = next < 32 ? (ends | (~has & 0x55555555u)) >> next : 0;
+    const int steps = stop ? (__ffs(stop) - 1) / 2 : (2 * W - next) / 2;
+    const bool last = state == 3 || (next < 32 && ((ends >> next) >> (2 * steps)) & 1);
+    const int parts = state == 3 ? 1 : 1 + steps + last;
+    if (begins) groups[__popc(starts & ((1u << lane) - 1))] = make_int4(lane, parts, last, 0);
+    const bool leaves = begins && !((lane & 1) && last);
+    const uint32_t left = __ballot_sync(~0u, leaves);
+    if (leaves) {
+      PartHeader h = hdr[lane >> 1][lane & 1];
+      h.state = last ? 3 : 1;
+      out_hdr[blockIdx.x * 2 + (lane & 1)] = h;
     }
-    const bool whole = begun && last == 3;
-    const int k = begun ? 1 : 0;
-    P* dst = out_part + blockIdx.x * 2 + k;
-    for (int e = tid; e < NT * W_::MT * 32; e += 32 * W) {
-      const int lane_e = e & 31, row = ((e >> 5) / W_::MT) * 8 + 2 * (lane_e & 3);
-      float m0 = -FLT_MAX, m1 = -FLT_MAX;
-      for (int c = 0; c < count; ++c) {
-        const P& p = part_of(c == 0 ? i : ((i >> 1) + c) * 2);
-        m0 = fmaxf(m0, p.m[row]);
-        m1 = fmaxf(m1, p.m[row + 1]);
-      }
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float l0 = 0.f, l1 = 0.f;
-      for (int c = 0; c < count; ++c) {
-        const P& p = part_of(c == 0 ? i : ((i >> 1) + c) * 2);
-        const float f0 = ex2(p.m[row] - m0), f1 = ex2(p.m[row + 1] - m1);
-        const float4 y = p.o[e];
-        o.x = fmaf(y.x, f0, o.x);
-        o.y = fmaf(y.y, f1, o.y);
-        o.z = fmaf(y.z, f0, o.z);
-        o.w = fmaf(y.w, f1, o.w);
-        l0 = fmaf(p.l[row], f0, l0);
-        l1 = fmaf(p.l[row + 1], f1, l1);
-      }
-      if (whole) {
-        write_merged<T, D, NT>(a, h.b, h.head, h.rb, e, o, l0, l1);
-      } else {
-        dst->o[e] = o;
-        if (((e >> 5) % W_::MT) == 0 && lane_e < 4) {
-          dst->m[row] = m0;
-          dst->m[row + 1] = m1;
-          dst->l[row] = l0;
-          dst->l[row + 1] = l1;
-        }
-      }
-    }
-    if (!whole) {
-      left[k] = true;
-      if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{last, h.b, h.head, h.rb};
-    }
-    // on to the last of these warps' part 1, which may begin another item
-    i += begun ? max(1, 2 * count - 2) : 2 * count - 1;
+    if (lane < 2 && !(left & (lane ? 0xAAAAAAAAu : 0x55555555u))) out_hdr[blockIdx.x * 2 + lane].state = 0;
   }
-  if (tid < 2 && !left[tid]) out_hdr[blockIdx.x * 2 + tid].state = 0;
+  __syncthreads();
+  constexpr int E = NT * W_::MT * 32;
+  for (int i = tid; i < __popc(starts) * E; i += 32 * W) {
+    const int4 gr = groups[i / E];
+    const int e = i % E, row = ((e >> 5) / W_::MT) * 8 + 2 * (e & 3);
+    Join join;
+    for (int c = 0; c < gr.y; ++c) {
+      const int w = (gr.x >> 1) + c;
+      const P& p = c == 0 && (gr.x & 1) ? *reinterpret_cast<const P*>(rings + w * kSlot) : heads[w];
+      join.add(p.o[e], *reinterpret_cast<const float2*>(&p.m[row]), *reinterpret_cast<const float2*>(&p.l[row]));
+    }
+    if ((gr.x & 1) && gr.z) {
+      write_merged<T, D, NT>(a, hdr[gr.x >> 1][1], e, join.o, join.l0, join.l1);
+    } else {
+      P* dst = out_part + blockIdx.x * 2 + (gr.x & 1);
+      dst->o[e] = join.o;
+      if ((e >> 5) % W_::MT == 0 && (e & 31) < 4) {
+        *reinterpret_cast<float2*>(&dst->m[row]) = make_float2(join.m0, join.m1);
+        *reinterpret_cast<float2*>(&dst->l[row]) = make_float2(join.l0, join.l1);
+      }
+    }
+  }
 }
 
 // Joins the parts of the items that span blocks: block c those of the item begun in block c of the
-// first kernel.
+// first kernel.  It is launched while the first one runs and waits for its end.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
   using P = Part<NT, D>;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const PartHeader* hdr = static_cast<const PartHeader*>(a.workspace);
   const P* part = reinterpret_cast<const P*>(static_cast<const uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
-  const int c0 = blockIdx.x;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const PartHeader h = hdr[c0 * 2 + 1];
   if (h.state != 1) return;
-  __shared__ int last;
-  if (threadIdx.x == 0) last = kCtas - 1;
-  __syncthreads();
-  for (int c = c0 + 1 + threadIdx.x; c < kCtas; c += blockDim.x)
-    if (hdr[c * 2].state == 3) atomicMin(&last, c);
-  __syncthreads();
-  const int end = last;
+  int end = kCtas - 1;  // the block that holds the item's last part
+  for (int c = c0 + 1; c < kCtas; c += 32) {
+    const uint32_t last = __ballot_sync(~0u, c + lane < kCtas && hdr[(c + lane) * 2].state == 3);
+    if (last) {
+      end = c + __ffs(last) - 1;
+      break;
+    }
+  }
   for (int e = threadIdx.x; e < NT * D / 16 * 32; e += blockDim.x) {
     const int row = ((e >> 5) / (D / 16)) * 8 + 2 * (e & 3);
-    const P* p0 = part + c0 * 2 + 1;
-    float m0 = p0->m[row], m1 = p0->m[row + 1];
-    for (int c = c0 + 1; c <= end; ++c) {
-      m0 = fmaxf(m0, part[c * 2].m[row]);
-      m1 = fmaxf(m1, part[c * 2].m[row + 1]);
+    Join join;
+    for (int c = c0; c <= end; c += 8) {
+      float4 o[8];
+      float2 m[8], l[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        m[i] = make_float2(-FLT_MAX, -FLT_MAX);
+        l[i] = make_float2(0.f, 0.f);
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c + i <= end) {
+          const P& p = part[(c + i) * 2 + (c + i == c0)];
+          o[i] = p.o[e];
+          m[i] = *reinterpret_cast<const float2*>(&p.m[row]);
+          l[i] = *reinterpret_cast<const float2*>(&p.l[row]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) join.add(o[i], m[i], l[i]);
     }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l0 = 0.f, l1 = 0.f;
-    for (int c = c0; c <= end; ++c) {
-      const P& p = c == c0 ? *p0 : part[c * 2];
-      const float f0 = ex2(p.m[row] - m0), f1 = ex2(p.m[row + 1] - m1);
-      const float4 y = p.o[e];
-      o.x = fmaf(y.x, f0, o.x);
-      o.y = fmaf(y.y, f1, o.y);
-      o.z = fmaf(y.z, f0, o.z);
-      o.w = fmaf(y.w, f1, o.w);
-      l0 = fmaf(p.l[row], f0, l0);
-      l1 = fmaf(p.l[row + 1], f1, l1);
-    }
-    write_merged<T, D, NT>(a, h.b, h.head, h.rb, e, o, l0, l1);
+    write_merged<T, D, NT>(a, h, e, join.o, join.l0, join.l1);
   }
 }
 
@@ -798,19 +843,28 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   using P = Part<NT, D>;
   constexpr int W = kWarpsOf<NT>;
   constexpr size_t ring = kStagesOf<D> * kChunk * unit_bytes(D, G), slot = ring > sizeof(P) ? ring : sizeof(P);
-  constexpr size_t rings = W * (slot + sizeof(P)), table = sizeof(int64_t) * kMaxRequests;
-  constexpr size_t bytes = rings > table ? rings : table;
+  constexpr size_t bytes = W * (slot + sizeof(P));
   static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
-  static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0, "parts are read in 16 bytes");
+  static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0 && 2 * kCtas * sizeof(PartHeader) % 16 == 0,
+                "parts are read in 16 bytes");
   cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   int shift = 4;
   while ((1 << shift) < a.page) ++shift;
-  attn_kernel<T, D, G, NT><<<kCtas, 32 * W, bytes, st>>>(a, shift);
+  attn_kernel<T, D, G, NT><<<kCtas, 32 * W, bytes, st>>>(a, shift, 1.0 / (kUnit * (a.hq / a.hkv)));
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  combine_kernel<T, D, NT><<<kCtas, 256, 0, st>>>(a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NT>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <typename T, int D, int G>
