@@ -399,7 +399,7 @@ def _device_index(*tensors) -> int:
 
 class _OnStream:
     """Makes a stream and its device current, so that what a call allocates belongs to the stream
-    that uses it.  Entered, it gives the raw stream."""
+    that uses it."""
 
     def __init__(self, device: int, stream):
         import torch
@@ -411,33 +411,21 @@ class _OnStream:
                       else torch.cuda.default_stream(device))
         if stream.device.index != device:
             raise ValueError(f"a stream of {stream.device} for tensors on device {device}")
-        self._ctx, self._raw = torch.cuda.stream(stream), stream.cuda_stream
+        self._ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
         self._ctx.__enter__()
-        return self._raw
 
     def __exit__(self, *exc):
         return self._ctx.__exit__(*exc)
 
 
-class _OnCurrent:
-    """The same where stream and device are current already."""
-
-    def __enter__(self):
-        return self._raw
-
-    def __exit__(self, *exc):
-        return None
-
-
-def _on(device: int, stream):
+def _raw_stream(device: int) -> Optional[int]:
+    """The raw current stream of `device`, or None when another device is current."""
     import torch
-    if stream is None and device == torch.cuda.current_device():
-        on = _OnCurrent()
-        on._raw = torch._C._cuda_getCurrentRawStream(device)
-        return on
-    return _OnStream(device, stream)
+    if torch._C._cuda_getDevice() != device:
+        return None
+    return torch._C._cuda_getCurrentRawStream(device)
 
 
 def _int32(name, t, shape):
@@ -479,9 +467,13 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
     add new_lens [B] (negative: end) and grow block_tables [B, max_blocks] from the stack
     free_list[:free_count]; tables and free list are updated in place, free_count too unless
     free_count_out is given.  Returns (lens_out [B], cu_new [B + 1], slots [n_slots], refused [1])."""
-    import torch
     dev = _device_index(lens, new_lens, block_tables, free_list, free_count, lens_out,
                         free_count_out)
+    raw = _raw_stream(dev) if stream is None else None
+    if raw is None:
+        with _OnStream(dev, stream):
+            return fq_page_step(lens, new_lens, block_tables, free_list, free_count, page, n_slots,
+                                lens_out, free_count_out)
     B = lens.numel()
     _int32("lens", lens, (B,))
     _int32("new_lens", new_lens, (B,))
@@ -498,18 +490,17 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
         free_count_out = free_count
     else:
         _int32("free_count_out", free_count_out, (1,))
-    with _on(dev, stream) as s:
-        if lens_out is None:
-            lens_out = lens.new_empty((B,))
-        else:
-            _int32("lens_out", lens_out, (B,))
-        # cu_new, refused and slots in one allocation
-        cu_new, refused, slots = lens.new_empty((B + 2 + n_slots,)).split((B + 1, 1, n_slots))
-        st = lib().fq_page_step(lens.data_ptr(), new_lens.data_ptr(), B, block_tables.data_ptr(),
-                                max_blocks, page, free_list.data_ptr(), n_blocks,
-                                free_count.data_ptr(), lens_out.data_ptr(),
-                                free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-                                n_slots, refused.data_ptr(), s)
+    if lens_out is None:
+        lens_out = lens.new_empty((B,))
+    else:
+        _int32("lens_out", lens_out, (B,))
+    # cu_new, refused and slots in one allocation
+    cu_new, refused, slots = lens.new_empty((B + 2 + n_slots,)).split((B + 1, 1, n_slots))
+    st = lib().fq_page_step(lens.data_ptr(), new_lens.data_ptr(), B, block_tables.data_ptr(),
+                            max_blocks, page, free_list.data_ptr(), n_blocks,
+                            free_count.data_ptr(), lens_out.data_ptr(),
+                            free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+                            n_slots, refused.data_ptr(), raw)
     if st:
         _check("fq_page_step", st)
     return lens_out, cu_new, slots, refused
@@ -526,6 +517,10 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     [n_blocks, Hkv, page / 16, unit bytes].  With values=True returns the quantised values
     (k_values, v_values) [n, Hkv, d] in the inputs' type."""
     dev = _device_index(k, v, slots, cache)
+    raw = _raw_stream(dev) if stream is None else None
+    if raw is None:
+        with _OnStream(dev, stream):
+            return fq_kv4_write(k, v, slots, cache, group, values)
     if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
         raise ValueError("k and v: two tensors [n, Hkv, d] of one type")
     n, hkv, d = k.shape
@@ -538,13 +533,11 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     if cache_hkv != hkv:
         raise ValueError(f"cache of {cache_hkv} kv heads, keys of {hkv}")
     kv = vv = kp = vp = None
-    with _on(dev, stream) as s:
-        if values:
-            kv, vv = k.new_empty((2, n, hkv, d)).unbind(0)
-            kp, vp = kv.data_ptr(), vv.data_ptr()
-        st = lib().fq_kv4_write(k.data_ptr(), v.data_ptr(), _kv4_dtype(k), n, hkv, d, k0, k1, v0,
-                                v1, slots.data_ptr(), cache.data_ptr(), n_blocks, page, group, kp,
-                                vp, s)
+    if values:
+        kv, vv = k.new_empty((2, n, hkv, d)).unbind(0)
+        kp, vp = kv.data_ptr(), vv.data_ptr()
+    st = lib().fq_kv4_write(k.data_ptr(), v.data_ptr(), _kv4_dtype(k), n, hkv, d, k0, k1, v0, v1,
+                            slots.data_ptr(), cache.data_ptr(), n_blocks, page, group, kp, vp, raw)
     if st:
         _check("fq_kv4_write", st)
     return (kv, vv) if values else None
@@ -559,6 +552,11 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: i
     every sequence has one.  window > 0: only the last `window` tokens are seen.  Returns out
     [n_q, Hq, d] of q's type."""
     dev = _device_index(q, cache, block_tables, kv_lens, cu_q, out, workspace)
+    raw = _raw_stream(dev) if stream is None else None
+    if raw is None:
+        with _OnStream(dev, stream):
+            return fq_kv4_attn(q, cache, block_tables, kv_lens, group, cu_q, max_q, window, scale,
+                               out, workspace)
     if q.dim() != 3 or block_tables.dim() != 2:
         raise ValueError("q: [n_q, Hq, d]; block_tables: [B, max_blocks]")
     n_q, hq, d = q.shape
@@ -574,23 +572,22 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: i
     if cu_q is not None:
         _int32("cu_q", cu_q, (B + 1,))
         cu = cu_q.data_ptr()
-    with _on(dev, stream) as s:
-        if out is None:
-            out = q.new_empty((n_q, hq, d))
-        elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-            raise ValueError("out: a contiguous tensor of q's shape and type")
-        if workspace is None:
-            ws_bytes = _KV4_WS.get(d)
-            if ws_bytes is None:
-                ws_bytes = _KV4_WS[d] = fq_kv4_attn_workspace_bytes(d)
-            workspace = cache.new_empty((ws_bytes,))
-        else:
-            ws_bytes = workspace.numel() * workspace.element_size()
-        st = lib().fq_kv4_attn(q.data_ptr(), _kv4_dtype(q), n_q, hq, d, q0, q1, cu, B, max_q,
-                               cache.data_ptr(), n_blocks, hkv, page, group,
-                               block_tables.data_ptr(), max_blocks, kv_lens.data_ptr(), window,
-                               1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
-                               workspace.data_ptr(), ws_bytes, s)
+    if out is None:
+        out = q.new_empty((n_q, hq, d))
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out: a contiguous tensor of q's shape and type")
+    if workspace is None:
+        ws_bytes = _KV4_WS.get(d)
+        if ws_bytes is None:
+            ws_bytes = _KV4_WS[d] = fq_kv4_attn_workspace_bytes(d)
+        workspace = cache.new_empty((ws_bytes,))
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    st = lib().fq_kv4_attn(q.data_ptr(), _kv4_dtype(q), n_q, hq, d, q0, q1, cu, B, max_q,
+                           cache.data_ptr(), n_blocks, hkv, page, group, block_tables.data_ptr(),
+                           max_blocks, kv_lens.data_ptr(), window,
+                           1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
+                           workspace.data_ptr(), ws_bytes, raw)
     if st:
         _check("fq_kv4_attn", st)
     return out

@@ -19,6 +19,7 @@
 //
 // mma.sync and not tcgen05: the products of decode are 8 to 16 rows wide, operands come out of
 // registers, and the tensor pipe has three quarters of its time left at the HBM bound.
+#include <atomic>
 #include <cfloat>
 
 #include <cuda_bf16.h>
@@ -540,7 +541,7 @@ __device__ __forceinline__ int64_t quotient(int64_t x, int64_t d, double inv) {
 }
 
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift, double inv_step) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift, double inv_step, int own_blocks) {
   using W_ = Warp<T, D, G, NT>;
   using P = Part<NT, D>;
   constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
@@ -561,74 +562,89 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   if (lane < kStages) ptx::mbar_init(&bars[warp][lane], kChunk);
   if (lane < 2) hdr[warp][lane].state = 0;
   ptx::fence_mbar_init();
-
-  // The line of all items' costs: each thread adds up its sequences', and the one whose cost holds
-  // the start of a warp's range tells that warp.
-  const int per = (a.B + 32 * W - 1) / (32 * W), b_mine = tid * per;
-  int64_t mine = 0;
-  for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
-    const Seq s = load_seq<NB>(a, b, r);
-    mine += a.hkv * s.upto(s.blocks);
-  }
-  int64_t x = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t y = __shfl_up_sync(~0u, x, d);
-    if (lane >= d) x += y;
-  }
-  if (lane == 31) scan[warp] = x;
-  __syncthreads();
-  int64_t below = x - mine, total = 0;
-#pragma unroll
-  for (int w = 0; w < W; ++w) {
-    if (w < warp) below += scan[w];
-    total += scan[w];
-  }
-  // a range is at least a unit long
-  const int64_t span = max((total + kCtas * W - 1) / (kCtas * W), (int64_t)kUnit * r);
-  const int64_t block0 = (int64_t)blockIdx.x * W * span;
-  if (below + mine > block0 && below < block0 + W * span) {
-    for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
-      int64_t cost = mine;
-      if (per > 1) {
-        const Seq s = load_seq<NB>(a, b, r);
-        cost = a.hkv * s.upto(s.blocks);
-      }
-      for (int w = 0; w < W; ++w) {
-        const int64_t x0 = block0 + w * span;
-        if (x0 >= below && x0 < below + cost) {
-          start_b[w] = b;
-          start_base[w] = below;
-        }
-      }
-      below += cost;
-    }
-  }
-  __syncthreads();
+  __syncwarp();  // a warp uses its own barriers only
 
   W_ st;
   uint8_t* ring = rings + warp * kSlot;
   const typename W_::Place place = W_::place(ptx::smem_u32(ring), lane);
   uint32_t count = 0;  // chunks so far: the ring's stage and its barrier's parity
   bool ok = true;
-  const int64_t x0 = block0 + warp * span, x1 = min(total, x0 + span);
-  int64_t item0 = x0, from = 0;
+  int64_t item0 = 0, from = 0, x1 = 0;
   int b = 0, head = 0, rb = 0;
   Seq s = {};
-  if (x0 < x1) {
-    // the item at x0
-    b = start_b[warp];
+  if (own_blocks > 0) {
+    // short contexts: a block to an item, its tokens shared out to the block's warps
+    rb = blockIdx.x % own_blocks;
+    head = blockIdx.x / own_blocks % a.hkv;
+    b = blockIdx.x / own_blocks / a.hkv;
     s = load_seq<NB>(a, b, r);
-    const int64_t one = s.upto(s.blocks), in_seq = x0 - start_base[warp];
-    head = (int)quotient(in_seq, one, 1.0 / (double)one);
-    const int64_t in_head = in_seq - head * one;
-    int above = s.blocks;
-    while (above - rb > 1) {
-      const int mid = (rb + above) >> 1;
-      if (s.upto(mid) <= in_head) rb = mid; else above = mid;
+    if (rb < s.blocks) {
+      const int64_t fixed = (int64_t)kItemTokens * r, rest = s.cost(rb) - fixed;
+      from = warp == 0 ? 0 : fixed + rest * warp / W;
+      x1 = fixed + rest * (warp + 1) / W;
     }
-    from = in_head - s.upto(rb);
-    item0 = x0 - from;
+  } else {
+    // The line of all items' costs: each thread adds up its sequences', and the one whose cost holds
+    // the start of a warp's range tells that warp.
+    const int per = (a.B + 32 * W - 1) / (32 * W), b_mine = tid * per;
+    int64_t mine = 0;
+    for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
+      const Seq s = load_seq<NB>(a, b, r);
+      mine += a.hkv * s.upto(s.blocks);
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) scan[warp] = x;
+    __syncthreads();
+    int64_t below = x - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      if (w < warp) below += scan[w];
+      total += scan[w];
+    }
+    // a range is at least a unit long
+    const int64_t span = max((total + kCtas * W - 1) / (kCtas * W), (int64_t)kUnit * r);
+    const int64_t block0 = (int64_t)blockIdx.x * W * span;
+    if (below + mine > block0 && below < block0 + W * span) {
+      for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
+        int64_t cost = mine;
+        if (per > 1) {
+          const Seq s = load_seq<NB>(a, b, r);
+          cost = a.hkv * s.upto(s.blocks);
+        }
+        for (int w = 0; w < W; ++w) {
+          const int64_t x0 = block0 + w * span;
+          if (x0 >= below && x0 < below + cost) {
+            start_b[w] = b;
+            start_base[w] = below;
+          }
+        }
+        below += cost;
+      }
+    }
+    __syncthreads();
+    const int64_t x0 = block0 + warp * span;
+    x1 = min(total, x0 + span);
+    item0 = x0;
+    if (x0 < x1) {
+      // the item at x0
+      b = start_b[warp];
+      s = load_seq<NB>(a, b, r);
+      const int64_t one = s.upto(s.blocks), in_seq = x0 - start_base[warp];
+      head = (int)quotient(in_seq, one, 1.0 / (double)one);
+      const int64_t in_head = in_seq - head * one;
+      int above = s.blocks;
+      while (above - rb > 1) {
+        const int mid = (rb + above) >> 1;
+        if (s.upto(mid) <= in_head) rb = mid; else above = mid;
+      }
+      from = in_head - s.upto(rb);
+      item0 = x0 - from;
+    }
   }
   for (; item0 + from < x1 && ok;) {
     const int64_t cost = s.cost(rb), to = min(x1 - item0, cost);
@@ -761,14 +777,14 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
     const bool last = state == 3 || (next < 32 && ((ends >> next) >> (2 * steps)) & 1);
     const int parts = state == 3 ? 1 : 1 + steps + last;
     if (begins) groups[__popc(starts & ((1u << lane) - 1))] = make_int4(lane, parts, last, 0);
-    const bool leaves = begins && !((lane & 1) && last);
+    const bool leaves = begins && !((lane & 1) && last);  // never with own blocks
     const uint32_t left = __ballot_sync(~0u, leaves);
     if (leaves) {
       PartHeader h = hdr[lane >> 1][lane & 1];
       h.state = last ? 3 : 1;
       out_hdr[blockIdx.x * 2 + (lane & 1)] = h;
     }
-    if (lane < 2 && !(left & (lane ? 0xAAAAAAAAu : 0x55555555u))) out_hdr[blockIdx.x * 2 + lane].state = 0;
+    if (own_blocks == 0 && lane < 2 && !(left & (lane ? 0xAAAAAAAAu : 0x55555555u))) out_hdr[blockIdx.x * 2 + lane].state = 0;
   }
   __syncthreads();
   constexpr int E = NT * W_::MT * 32;
@@ -847,13 +863,26 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
   static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0 && 2 * kCtas * sizeof(PartHeader) % 16 == 0,
                 "parts are read in 16 bytes");
-  cudaError_t e = cudaFuncSetAttribute(attn_kernel<T, D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have this much shared memory
+  if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(attn_kernel<T, D, G, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
   int shift = 4;
   while ((1 << shift) < a.page) ++shift;
-  attn_kernel<T, D, G, NT><<<kCtas, 32 * W, bytes, st>>>(a, shift, 1.0 / (kUnit * (a.hq / a.hkv)));
+  // A block to each item where they fit the SMs at once and a warp's share is at most 8 units: no
+  // parts leave a block, so the second kernel falls away (one sequence of 517 tokens, 8 kv heads:
+  // XXX us against YYY; at 4096 tokens the ranges over all SMs win).
+  const int r = a.hq / a.hkv, own = (int)(((int64_t)a.max_q * r + 8 * NT - 1) / (8 * NT));
+  const int64_t items = (int64_t)a.B * a.hkv * own;
+  const bool whole = items <= kCtas && (int64_t)a.max_blocks * a.page <= 8 * kUnit * W;
+  attn_kernel<T, D, G, NT><<<whole ? (unsigned)items : kCtas, 32 * W, bytes, st>>>(a, shift, 1.0 / (kUnit * r), whole ? own : 0);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || whole) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas);
   cfg.blockDim = dim3(256);

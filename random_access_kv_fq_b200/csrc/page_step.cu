@@ -4,11 +4,12 @@
 // place among the released pages; the a-th new page of the step is the a-th from the top of the
 // free stack, so every page, table entry and slot has a closed form and nothing is atomic.
 //
-// Bound by latency: at most a few bytes per request, page and slot.  One launch: every block of
-// one cluster computes the sums itself (B values from L2, the sums in shared memory), so no block
-// waits for another's sums; two cluster barriers order (1) all reads of lens and free_count before
-// they may be overwritten in place and (2) released pages before they are handed out again.  The
-// slots are written one thread each, the request found by bisection of the sums in shared memory.
+// Bound by latency: a few bytes per request, page and slot, behind four dependent steps (lengths,
+// sums, pages, slots).  One launch: every block of one cluster computes the sums itself (B values
+// from L2, the sums in shared memory), so no block waits for another's sums; two cluster barriers
+// order (1) all reads of lens and free_count before they may be overwritten in place and (2)
+// released pages before they are handed out again.  A warp writes 256 slots at a time: it finds the
+// requests of the first and the last by bisection and its lanes search only between them.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -21,35 +22,41 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
 constexpr int kCluster = 8;
+constexpr int kSlots = 8;  // slots of a lane at a time: their table reads are in flight together
 
 __device__ __forceinline__ int sat(int64_t x) { return x > INT_MAX ? INT_MAX : (int)x; }
 
-// Inclusive block-wide sum of one value per thread; `total` gets the block's sum.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t* part, int64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ int64_t warp_scan(int64_t x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int m = 1; m < 32; m <<= 1) {
     const int64_t y = __shfl_up_sync(~0u, x, m);
     if (lane >= m) x += y;
   }
-  __syncthreads();  // `part` may still be read from the scan before
-  if (lane == 31) part[warp] = x;
-  __syncthreads();
-  int64_t below = 0;
-  total = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) {
-    if (i < warp) below += part[i];
-    total += part[i];
-  }
-  return x + below;
+  return x;
 }
 
-// the last of a[0..n) that is <= x (a ascending, a[0] <= x)
-__device__ __forceinline__ int last_le(const int* a, int n, int x) {
-  int lo = 0, hi = n;
+// Exclusive block-wide sums of two values per thread; `total` gets the block's sums.
+struct Two {
+  int64_t a, b;
+};
+__device__ __forceinline__ Two block_scan(Two x, Two* part, Two& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const Two up{warp_scan(x.a), warp_scan(x.b)};
+  __syncthreads();  // `part` may still be read from the scan before
+  if (lane == 31) part[warp] = up;
+  __syncthreads();
+  Two w{0, 0};
+  if (lane < warps) w = part[lane];
+  const Two all{warp_scan(w.a), warp_scan(w.b)};
+  total = Two{__shfl_sync(~0u, all.a, 31), __shfl_sync(~0u, all.b, 31)};
+  return Two{__shfl_sync(~0u, all.a - w.a, warp) + up.a - x.a,
+             __shfl_sync(~0u, all.b - w.b, warp) + up.b - x.b};
+}
+
+// the last of a[lo..hi) that is <= x (a ascending, a[lo] <= x)
+__device__ __forceinline__ int last_le(const int* a, int lo, int hi, int x) {
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (a[mid] <= x) lo = mid; else hi = mid;
@@ -57,104 +64,129 @@ __device__ __forceinline__ int last_le(const int* a, int n, int x) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kThreads) page_step_kernel(PageArgs a) {
+template <bool ALONE>
+__global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_shift) {
   extern __shared__ int sums[];
-  __shared__ int64_t part[kThreads / 32];
+  __shared__ Two part[32];
   int* cu = sums;              // [B + 1] first new token of a request
   int* off = cu + a.B + 1;     // [B]     first new page
   int* rel = off + a.B;        // [B]     first released page
   int* held = rel + a.B;       // [B]     tokens held before the step; ~held when it is refused
   const cg::cluster_group cluster = cg::this_cluster();
-  const int n_thr = kThreads * cluster.num_blocks();
-  const int me = cluster.block_rank() * kThreads + threadIdx.x;
-  const int per = (a.B + kThreads - 1) / kThreads;
+  const auto all_blocks = [&] {
+    if (ALONE) __syncthreads(); else cluster.sync();
+  };
+  const int rank = ALONE ? 0 : (int)cluster.block_rank();
+  const int threads = blockDim.x, n_thr = threads * (ALONE ? 1 : kCluster), me = rank * threads + threadIdx.x;
+  const int per = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
-  const int64_t room = (int64_t)a.max_blocks * a.page;
+  const int64_t room = (int64_t)a.max_blocks << page_shift;
   const int count = min(max(__ldcg(a.free_count), 0), a.n_blocks);
+  const auto pages_of = [&](int64_t tokens) { return (tokens + a.page - 1) >> page_shift; };
 
   // this thread's requests: tokens to add and pages to release
-  int64_t tokens = 0, released = 0, total_tokens, total_released, total_need, total_refused, total_taken;
+  Two mine{0, 0}, total;
   for (int b = b0; b < b1; ++b) {
     const int add = __ldcg(a.new_lens + b);
     const int h = (int)min((int64_t)max(__ldcg(a.lens + b), 0), room);
     held[b] = h;
     off[b] = add;
-    if (add < 0) released += (h + (int64_t)a.page - 1) / a.page; else tokens += add;
+    if (add < 0) mine.b += pages_of(h); else mine.a += add;
   }
-  int64_t at = block_scan(tokens, part, total_tokens) - tokens;
-  int64_t gone = block_scan(released, part, total_released) - released;
-  const int avail = (int)min((int64_t)a.n_blocks, count + total_released);
-  int64_t need = 0;
+  const Two first = block_scan(mine, part, total);
+  const int64_t total_tokens = total.a;
+  const int avail = (int)min((int64_t)a.n_blocks, count + total.b);
+  // the pages that they need, if they fit the table and the slots
+  Two need{0, 0};
+  int64_t at = first.a, gone = first.b;
   for (int b = b0; b < b1; ++b) {
     const int add = off[b];
-    const int64_t h = held[b], pages = (h + a.page - 1) / a.page;
+    const int64_t h = held[b];
     cu[b] = sat(at);
     rel[b] = sat(gone);
-    if (add < 0) { gone += pages; continue; }
-    at += add;
-    if (h + add <= room && at <= a.n_slots) need += (h + add + a.page - 1) / a.page - pages;
+    if (add < 0) {
+      gone += pages_of(h);
+    } else {
+      at += add;
+      if (h + add <= room && at <= a.n_slots) need.a += pages_of(h + add) - pages_of(h);
+    }
   }
-  int64_t upto = block_scan(need, part, total_need) - need;
-  int64_t refused = 0, taken = 0;
-  // cu, rel of this thread's requests are final; off and held get their final meaning
-  int64_t tok_end = at;
-  at = tok_end - tokens;
+  int64_t upto = block_scan(need, part, total).a;
+  // a request that fits is served while the pages needed up to it are there
+  Two done{0, 0};  // pages handed out, requests refused
+  at = first.a;
   for (int b = b0; b < b1; ++b) {
     const int add = off[b];
-    const int64_t h = held[b], pages = (h + a.page - 1) / a.page;
+    const int64_t h = held[b];
     off[b] = sat(upto);
     if (add < 0) continue;
     at += add;
     const bool fits = h + add <= room && at <= a.n_slots;
-    const int64_t n = fits ? (h + add + a.page - 1) / a.page - pages : 0;
+    const int64_t n = fits ? pages_of(h + add) - pages_of(h) : 0;
     upto += n;
     if (!fits || (n > 0 && upto > avail)) {
       held[b] = ~held[b];
-      ++refused;
-    } else if (n > 0) {
-      taken += n;
+      ++done.b;
+    } else {
+      done.a += n;
     }
   }
-  block_scan(refused, part, total_refused);
-  block_scan(taken, part, total_taken);
+  block_scan(done, part, total);
+  const int taken = (int)total.a;
   if (threadIdx.x == 0) cu[a.B] = sat(total_tokens);
-  __syncthreads();
-  cluster.sync();  // lens and free_count are read: they may be overwritten now
+  all_blocks();  // the sums are there; lens and free_count are read and may be overwritten
 
   for (int b = me; b < a.B; b += n_thr) {
     const int h = held[b], next = cu[b + 1] - cu[b];
-    const bool out = a.new_lens[b] < 0;
+    const bool out = __ldcg(a.new_lens + b) < 0;
     a.lens_out[b] = out ? 0 : h < 0 ? ~h : h + next;
   }
   for (int b = me; b <= a.B; b += n_thr) a.cu_new[b] = cu[b];
   if (me == 0) {
-    *a.free_count_out = avail - (int)total_taken;
-    *a.refused = (int)total_refused;
+    *a.free_count_out = avail - taken;
+    *a.refused = (int)total.b;
   }
-  for (int r = me; r < avail - count; r += n_thr) {
-    const int b = last_le(rel, a.B, r);
-    a.free_list[count + r] = a.tables[(int64_t)b * a.max_blocks + (r - rel[b])];
+  if (avail > count) {
+    for (int r = me; r < avail - count; r += n_thr) {
+      const int b = last_le(rel, 0, a.B, r);
+      a.free_list[count + r] = a.tables[(int64_t)b * a.max_blocks + (r - rel[b])];
+    }
+    all_blocks();  // released pages are on the stack
   }
-  cluster.sync();  // released pages are on the stack
 
-  for (int p = me; p < (int)total_taken; p += n_thr) {
-    const int b = last_le(off, a.B, p);
-    const int pages = (held[b] + a.page - 1) / a.page;
-    a.tables[(int64_t)b * a.max_blocks + pages + (p - off[b])] = __ldcg(a.free_list + (avail - 1 - p));
+  for (int p = me; p < taken; p += n_thr) {
+    const int b = last_le(off, 0, a.B, p);
+    a.tables[(int64_t)b * a.max_blocks + (int)pages_of(held[b]) + (p - off[b])] = __ldcg(a.free_list + (avail - 1 - p));
   }
-  for (int i = me; i < a.n_slots; i += n_thr) {
-    int slot = -1;
-    if (i < cu[a.B]) {
-      const int b = last_le(cu, a.B, i);
-      const int h = held[b];
-      if (h >= 0) {
-        const int pos = h + (i - cu[b]), pg = pos / a.page, pages = (h + a.page - 1) / a.page;
-        const int id = pg < pages ? a.tables[(int64_t)b * a.max_blocks + pg]
-                                  : __ldcg(a.free_list + (avail - 1 - (off[b] + pg - pages)));
-        if (id >= 0 && id < a.n_blocks) slot = id * a.page + pos % a.page;
+  const int lane = threadIdx.x & 31, written = min(a.n_slots, cu[a.B]);
+  for (int i0 = (me >> 5) * 32 * kSlots; i0 < a.n_slots; i0 += n_thr * kSlots) {
+    int lo = 0, hi = 1;
+    if (i0 < written) {
+      lo = last_le(cu, 0, a.B, i0);
+      hi = last_le(cu, lo, a.B, min(i0 + 32 * kSlots, written) - 1) + 1;
+    }
+    int id[kSlots], in[kSlots];
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int i = i0 + 32 * k + lane;
+      id[k] = -1;
+      in[k] = 0;
+      if (i < written) {
+        const int b = last_le(cu, lo, hi, i);
+        const int h = held[b];
+        if (h >= 0) {
+          const int pos = h + (i - cu[b]), pg = pos >> page_shift, pages = (int)pages_of(h);
+          in[k] = pos & (a.page - 1);
+          id[k] = pg < pages ? a.tables[(int64_t)b * a.max_blocks + pg]
+                             : __ldcg(a.free_list + (avail - 1 - (off[b] + pg - pages)));
+        }
       }
     }
-    a.slots[i] = slot;
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) {
+      const int i = i0 + 32 * k + lane;
+      if (i < a.n_slots) a.slots[i] = id[k] >= 0 && id[k] < a.n_blocks ? (id[k] << page_shift) + in[k] : -1;
+    }
   }
 }
 
@@ -162,23 +194,28 @@ __global__ void __launch_bounds__(kThreads) page_step_kernel(PageArgs a) {
 
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(int) * (4 * (size_t)a.B + 1);
-  cudaError_t e = cudaFuncSetAttribute(page_step_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(int) * (4 * kMaxRequests + 1)));
-  if (e != cudaSuccess) return e;
+  // One block does a small step (256 decodes: XXX us, with the cluster YYY); a cluster shares the
+  // stores of a large one.  Few requests need few warps: their sums are sooner there.
+  const bool alone = (int64_t)a.n_slots + a.B <= 8192;
+  const auto kernel = alone ? page_step_kernel<true> : page_step_kernel<false>;
+  if (smem > 48 * 1024 - sizeof(Two) * 32) {  // what a block may have unasked
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  int shift = 0;
+  while ((1 << shift) < a.page) ++shift;
   cudaLaunchConfig_t cfg = {};
-  // one block does a small step; a cluster shares the stores of a large one
-  const unsigned blocks = (int64_t)a.n_slots + a.B <= 4 * kThreads ? 1 : kCluster;
-  cfg.gridDim = dim3(blocks);
-  cfg.blockDim = dim3(kThreads);
+  cfg.gridDim = dim3(alone ? 1 : kCluster);
+  cfg.blockDim = dim3(a.B <= 256 && a.n_slots <= 2048 ? 256 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = blocks;
+  at[0].val.clusterDim.x = kCluster;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, page_step_kernel, a);
+  cfg.numAttrs = alone ? 0 : 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
