@@ -37,10 +37,11 @@ __device__ unsigned int g_kv4_wait_timeouts = 0;  // blocks whose bounded waits 
 
 constexpr int kCtas = 148;       // one block per SM
 constexpr int kChunk = 2;        // units of a stage of a warp's ring: one wait for 32 tokens
-constexpr int kItemTokens = 48;  // an item's fixed cost, in tokens (its queries and its end)
+constexpr int kItemUnits = 3;    // an item's fixed cost, in units (its queries and its end)
 
-template <int NT>
-constexpr int kWarpsOf = NT == 1 ? 16 : 12;
+// warps of a block, by the registers that their accumulators leave
+template <int NT, int D>
+constexpr int kWarpsOf = NT == 1 ? 16 : D == 64 ? 12 : 8;
 // stages of a ring: ~10 KB a warp, 160 KB of an SM's copies in flight or in use
 template <int D>
 constexpr int kStagesOf = D == 64 ? 4 : 2;
@@ -61,34 +62,25 @@ struct Part {
 
 struct Seq {
   int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
-  int64_t k0;                  // cost of row block rb: k0 + slope (rb + 1), in 1 / (hq / hkv) tokens
-  int slope;
-  __device__ int64_t cost(int rb) const { return k0 + (int64_t)slope * (rb + 1); }
-  __device__ int64_t upto(int rb) const { return rb * k0 + (int64_t)slope * rb * (rb + 1) / 2; }
+  int cost;                    // of each of its row blocks, in units: the most that one may see
 };
 
 template <int NB>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   Seq s;
-  const int64_t room = (int64_t)a.max_blocks * a.page;
-  s.n = (int)min((int64_t)max(__ldg(a.kv_lens + b), 0), room);
+  s.n = min(max(__ldg(a.kv_lens + b), 0), a.max_blocks * a.page);
   s.q0 = b;
   s.m = 1;
   if (a.cu_q) {
     s.q0 = __ldg(a.cu_q + b);
     s.m = max(0, min(__ldg(a.cu_q + b + 1) - s.q0, a.max_q));
-    if (s.q0 < 0 || (int64_t)s.q0 + s.m > a.n_q) s.m = 0;
+    if (s.q0 < 0 || s.q0 > a.n_q - s.m) s.m = 0;
   }
   s.rows = s.m * r;
   s.blocks = (s.rows + NB - 1) / NB;
-  // an upper bound of the tokens that each row block sees, linear in the row block
-  if (a.window > 0) {
-    s.k0 = (int64_t)r * (kItemTokens + 32 + min((int64_t)s.n, (int64_t)a.window + NB));
-    s.slope = 0;
-  } else {
-    s.k0 = (int64_t)r * (kItemTokens + 16 + max(s.n - s.m + 1, 0));
-    s.slope = NB;
-  }
+  s.cost = s.n;
+  if (a.window > 0) s.cost = min(s.n, min(a.window, 1 << 30) + NB + kUnit);
+  s.cost = (s.cost + kUnit - 1) / kUnit + kItemUnits;
   return s;
 }
 
@@ -533,25 +525,18 @@ struct Join {
   }
 };
 
-// floor(x / d) for 0 <= x < 2^52, given 1 / d
-__device__ __forceinline__ int64_t quotient(int64_t x, int64_t d, double inv) {
-  int64_t q = (int64_t)((double)x * inv);
-  const int64_t rest = x - q * d;
-  return rest < 0 ? q - 1 : rest >= d ? q + 1 : q;
-}
-
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, int page_shift, double inv_step, int own_blocks) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs a, int page_shift, int own_blocks) {
   using W_ = Warp<T, D, G, NT>;
   using P = Part<NT, D>;
-  constexpr int W = kWarpsOf<NT>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
+  constexpr int W = kWarpsOf<NT, D>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
   constexpr size_t kRing = kStages * kChunk * UB, kSlot = kRing > sizeof(P) ? kRing : sizeof(P);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* rings = smem;                                          // [W][kSlot]
   P* heads = reinterpret_cast<P*>(smem + W * kSlot);              // [W]
   __shared__ uint64_t bars[W][kStages];
   __shared__ PartHeader hdr[W][2];
-  __shared__ int64_t scan[W], start_base[W];
+  __shared__ int64_t scan[W], start_in[W];
   __shared__ int start_b[W];
   __shared__ int4 groups[2 * W];
   __shared__ int gave_up;
@@ -569,28 +554,30 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
   const typename W_::Place place = W_::place(ptx::smem_u32(ring), lane);
   uint32_t count = 0;  // chunks so far: the ring's stage and its barrier's parity
   bool ok = true;
-  int64_t item0 = 0, from = 0, x1 = 0;
-  int b = 0, head = 0, rb = 0;
+  // What is left of this warp's range of the line, where it begins in its first item, and that item:
+  // number `block` of the row blocks of (sequence b, kv head).
+  int64_t left = 0;
+  int from = 0, b = 0, head = 0, block = 0;
   Seq s = {};
   if (own_blocks > 0) {
-    // short contexts: a block to an item, its tokens shared out to the block's warps
-    rb = blockIdx.x % own_blocks;
+    // short contexts: a block to an item, shared out to its warps
+    block = blockIdx.x % own_blocks;
     head = blockIdx.x / own_blocks % a.hkv;
     b = blockIdx.x / own_blocks / a.hkv;
     s = load_seq<NB>(a, b, r);
-    if (rb < s.blocks) {
-      const int64_t fixed = (int64_t)kItemTokens * r, rest = s.cost(rb) - fixed;
-      from = warp == 0 ? 0 : fixed + rest * warp / W;
-      x1 = fixed + rest * (warp + 1) / W;
+    if (block < s.blocks) {
+      s.cost = kItemUnits + W;  // a W-th of the units each, whatever their number
+      from = warp == 0 ? 0 : kItemUnits + warp;
+      left = warp == 0 ? kItemUnits + 1 : 1;
     }
   } else {
-    // The line of all items' costs: each thread adds up its sequences', and the one whose cost holds
-    // the start of a warp's range tells that warp.
-    const int per = (a.B + 32 * W - 1) / (32 * W), b_mine = tid * per;
+    // The line of all items' costs: each thread adds up its sequences', and the one whose cost
+    // holds the start of a warp's range tells that warp.
+    const int per = (a.B + 32 * W - 1) / (32 * W), b0 = tid * per, b1 = min(a.B, b0 + per);
     int64_t mine = 0;
-    for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
-      const Seq s = load_seq<NB>(a, b, r);
-      mine += a.hkv * s.upto(s.blocks);
+    for (int i = b0; i < b1; ++i) {
+      s = load_seq<NB>(a, i, r);
+      mine += (int64_t)(a.hkv * s.blocks) * s.cost;
     }
     int64_t x = mine;
 #pragma unroll
@@ -601,53 +588,51 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
     if (lane == 31) scan[warp] = x;
     __syncthreads();
     int64_t below = x - mine, total = 0;
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < W; ++w) {
       if (w < warp) below += scan[w];
       total += scan[w];
     }
-    // a range is at least a unit long
-    const int64_t span = max((total + kCtas * W - 1) / (kCtas * W), (int64_t)kUnit * r);
+    const int64_t span = max((int64_t)(total * (1.0 / (kCtas * W))) + 1, (int64_t)kChunk);
     const int64_t block0 = (int64_t)blockIdx.x * W * span;
     if (below + mine > block0 && below < block0 + W * span) {
-      for (int b = b_mine; b < min(a.B, b_mine + per); ++b) {
-        int64_t cost = mine;
+      for (int i = b0; i < b1; ++i) {
         if (per > 1) {
-          const Seq s = load_seq<NB>(a, b, r);
-          cost = a.hkv * s.upto(s.blocks);
+          s = load_seq<NB>(a, i, r);
+          mine = (int64_t)(a.hkv * s.blocks) * s.cost;
         }
+#pragma unroll 1
         for (int w = 0; w < W; ++w) {
-          const int64_t x0 = block0 + w * span;
-          if (x0 >= below && x0 < below + cost) {
-            start_b[w] = b;
-            start_base[w] = below;
+          const int64_t x0 = block0 + w * span - below;
+          if (x0 >= 0 && x0 < mine) {
+            start_b[w] = i;
+            start_in[w] = x0;
           }
         }
-        below += cost;
+        below += mine;
       }
     }
     __syncthreads();
-    const int64_t x0 = block0 + warp * span;
-    x1 = min(total, x0 + span);
-    item0 = x0;
-    if (x0 < x1) {
-      // the item at x0
+    left = min(span, total - block0 - warp * span);
+    if (left > 0) {
       b = start_b[warp];
       s = load_seq<NB>(a, b, r);
-      const int64_t one = s.upto(s.blocks), in_seq = x0 - start_base[warp];
-      head = (int)quotient(in_seq, one, 1.0 / (double)one);
-      const int64_t in_head = in_seq - head * one;
-      int above = s.blocks;
-      while (above - rb > 1) {
-        const int mid = (rb + above) >> 1;
-        if (s.upto(mid) <= in_head) rb = mid; else above = mid;
-      }
-      from = in_head - s.upto(rb);
-      item0 = x0 - from;
+      const int64_t in_seq = start_in[warp];
+      // which of the sequence's items, all of one cost; the estimate is off by one at most
+      int64_t item = (int64_t)((double)in_seq / s.cost);
+      if (item * s.cost > in_seq) --item;
+      if (in_seq - item * s.cost >= s.cost) ++item;
+      from = (int)(in_seq - item * s.cost);
+      head = (int)item / s.blocks;
+      block = (int)item - head * s.blocks;
     }
   }
-  for (; item0 + from < x1 && ok;) {
-    const int64_t cost = s.cost(rb), to = min(x1 - item0, cost);
+  while (left > 0 && ok) {
+    const int to = (int)min((int64_t)s.cost, from + left);
+    left -= to - from;
+    // Row blocks from both ends in turn: later ones see more tokens, two neighbours about as many as
+    // any two.
+    const int rb = block & 1 ? s.blocks - 1 - (block >> 1) : block >> 1;
     // tokens that any row of the block sees, in units; the part of them in this range
     const int past = s.n - s.m + 1;
     const uint32_t row0 = rb * NB, row1 = min(rb * NB + NB, s.rows) - 1;
@@ -655,9 +640,13 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
     const int end = max(0, past + tok1);
     const int first = a.window > 0 ? max(0, past + tok0 - a.window) : 0;
     const int base_u = first / kUnit, units = end > first ? (end + kUnit - 1) / kUnit - base_u : 0;
-    const int64_t fixed = (int64_t)kItemTokens * r, step = (int64_t)kUnit * r;
-    const int u0 = from <= fixed ? 0 : (int)min((int64_t)units, quotient(from - fixed + step - 1, step, inv_step));
-    const int u1 = to == cost ? units : to <= fixed ? 0 : (int)min((int64_t)units, quotient(to - fixed + step - 1, step, inv_step));
+    const int full = s.cost - kItemUnits;
+    const float ratio = (float)units / (float)full;
+    const auto share = [&](int x) {
+      x -= kItemUnits;
+      return x <= 0 ? 0 : x >= full ? units : units == full ? x : min(units, (int)(x * ratio));
+    };
+    const int u0 = share(from), u1 = share(to);
 
     st.reset();
     if (u0 < u1) {
@@ -695,6 +684,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
       st.fetch_queries(a, s, head, rb, r, lane);
       for (int j = 0; j < chunks && j < kStages; ++j) issue(j);
       st.convert_queries(a, s, rb, r, lane);
+      // a few units go through the code that checks each token: less code to fetch
+      const bool clean = chunks > 2;
       const int all_end = past + tok0, all_first = a.window > 0 ? past + tok1 - a.window : 0;
       // a wait that gives up ends the loop once the copies in flight had their time to land
       int landing = chunks;
@@ -715,7 +706,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
           u.ks += off;
           u.v += off;
           u.vs += off;
-          if (pos0 >= all_first && pos0 + kChunk * kUnit <= all_end && skip == 0) {
+          if (clean && pos0 >= all_first && pos0 + kChunk * kUnit <= all_end && skip == 0) {
 #pragma unroll
             for (int i = 0; i < kChunk; ++i)
               st.template unit<false>(typename W_::Place{u.k + i * UB, u.ks + i * UB, u.v + i * UB, u.vs + i * UB}, 0, 0, 0, lane);
@@ -736,22 +727,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT>, 1) attn_kernel(AttnArgs a, 
       count += chunks;
       st.finish_sums();
     }
-    if (from == 0 && to == cost) {
+    if (from == 0 && to == s.cost) {
       st.write_out(a, s, head, rb, r, lane);
     } else {
       // an item begun before this range leaves its part beside the ring, one that goes on in it
       const int k = from > 0 ? 0 : 1;
       st.write_part(k == 0 ? heads + warp : reinterpret_cast<P*>(ring), lane);
-      if (lane == 0) hdr[warp][k] = PartHeader{to == cost ? 3 : 1, s.q0, s.rows, head, rb};
+      if (lane == 0) hdr[warp][k] = PartHeader{to == s.cost ? 3 : 1, s.q0, s.rows, head, rb};
     }
     // the next item of the line
-    item0 += cost;
     from = 0;
-    if (++rb == s.blocks) {
-      rb = 0;
+    if (left > 0 && ++block == s.blocks) {
+      block = 0;
       if (++head == a.hkv) {
         head = 0;
-        if (item0 < x1) do s = load_seq<NB>(a, ++b, r); while (s.blocks == 0);
+        do s = load_seq<NB>(a, ++b, r); while (s.blocks == 0);
       }
     }
   }
@@ -857,7 +847,7 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
 template <typename T, int D, int G, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   using P = Part<NT, D>;
-  constexpr int W = kWarpsOf<NT>;
+  constexpr int W = kWarpsOf<NT, D>;
   constexpr size_t ring = kStagesOf<D> * kChunk * unit_bytes(D, G), slot = ring > sizeof(P) ? ring : sizeof(P);
   constexpr size_t bytes = W * (slot + sizeof(P));
   static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
@@ -880,7 +870,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   const int r = a.hq / a.hkv, own = (int)(((int64_t)a.max_q * r + 8 * NT - 1) / (8 * NT));
   const int64_t items = (int64_t)a.B * a.hkv * own;
   const bool whole = items <= kCtas && (int64_t)a.max_blocks * a.page <= 8 * kUnit * W;
-  attn_kernel<T, D, G, NT><<<whole ? (unsigned)items : kCtas, 32 * W, bytes, st>>>(a, shift, 1.0 / (kUnit * r), whole ? own : 0);
+  attn_kernel<T, D, G, NT><<<whole ? (unsigned)items : kCtas, 32 * W, bytes, st>>>(a, shift, whole ? own : 0);
   e = cudaGetLastError();
   if (e != cudaSuccess || whole) return e;
   cudaLaunchConfig_t cfg = {};

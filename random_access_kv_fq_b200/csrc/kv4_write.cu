@@ -5,10 +5,12 @@
 // (c = 0 where s = 0); the cache then stands for c s + z.  The record keeps z and s in 16 bits, so
 // the codes are taken against the rounded z and s: what is lost to their rounding is not lost twice.
 //
-// Bound by HBM: 2 d elements in, d + 8 d / G bytes out per (token, kv head), ~15 instructions per
-// element.  One thread takes 8 coordinates (a 16-byte load and one 32-bit word of codes) of a
-// token's key and of its value, a block the same kv head of 2048 / d consecutive tokens, whose
-// rows share units: their 4-byte stores join to whole sectors in L2.
+// Bound by HBM: 2 d elements in, d + 8 d / G bytes out (and 2 d elements with the values) per (token,
+// kv head).  One thread takes 8 coordinates (a 16-byte load and one 32-bit word of codes) of a
+// token's key and of its value; a block takes the same kv head of 2048 / d consecutive tokens, whose
+// rows share units: their 4-byte stores join to whole sectors in L2.  What it computes is kept to
+// about 13 instructions per element, or it would be bound by their issue: rounding and clamping on
+// floats (adding 1.5 2^23 rounds to the nearest even integer), codes joined by exact FMAs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -29,15 +31,6 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 template <>
 __device__ __forceinline__ float to_float(float x) { return x; }
 template <typename T>
-__device__ __forceinline__ T from_float(float x);
-template <>
-__device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
-template <>
-__device__ __forceinline__ float from_float(float x) { return x; }
-
-template <typename T>
 struct alignas(16) Pack {
   T x[8];
 };
@@ -57,16 +50,21 @@ __device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
   }
 }
 
+__device__ __forceinline__ uint32_t pack2(__half, float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 // Quantises this thread's 8 coordinates with the other lanes of its group; returns the code word
 // and, in `sz`, the group's s (low half) and z.
 template <typename T, int G>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, T* values) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-  }
+  float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
+  float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 #pragma unroll
   for (int m = 1; m < G / 8; m <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(~0u, lo, m));
@@ -78,42 +76,52 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, 
   const float s = __half2float(s16);
   const float inv = s > 0.f ? 1.0f / s : 0.f;
   sz = (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(z16) << 16);
-  uint32_t word = 0;
-  Pack<T> out;
+  const float magic = 12582912.f;  // 1.5 2^23: what is added to it is rounded to an integer
+  float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float c = fminf(fmaxf(rintf((x[i] - z) * inv), 0.f), 15.f);
-    word |= (uint32_t)c << (4 * i);
-    out.x[i] = from_float<T>(fmaf(c, s, z));
-  }
+  for (int i = 0; i < 8; ++i)
+    c[i] = __fadd_rn(__fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], z), inv), 0.f), 15.f), magic), -magic);
   if (values) {
-    uint4* w = reinterpret_cast<uint4*>(&out);
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(out) / 16; ++i) reinterpret_cast<uint4*>(values)[i] = w[i];
+      for (int i = 0; i < 2; ++i)
+        reinterpret_cast<float4*>(values)[i] = make_float4(fmaf(c[4 * i], s, z), fmaf(c[4 * i + 1], s, z),
+                                                           fmaf(c[4 * i + 2], s, z), fmaf(c[4 * i + 3], s, z));
+    } else {
+      uint4 w;
+      w.x = pack2(T{}, fmaf(c[0], s, z), fmaf(c[1], s, z));
+      w.y = pack2(T{}, fmaf(c[2], s, z), fmaf(c[3], s, z));
+      w.z = pack2(T{}, fmaf(c[4], s, z), fmaf(c[5], s, z));
+      w.w = pack2(T{}, fmaf(c[6], s, z), fmaf(c[7], s, z));
+      *reinterpret_cast<uint4*>(values) = w;
+    }
   }
-  return word;
+  // four codes in the low 16 bits of a float between 2^23 and 2^24
+  const float low = fmaf(c[3], 4096.f, fmaf(c[2], 256.f, fmaf(c[1], 16.f, c[0] + 8388608.f)));
+  const float high = fmaf(c[7], 4096.f, fmaf(c[6], 256.f, fmaf(c[5], 16.f, c[4] + 8388608.f)));
+  return __byte_perm(__float_as_uint(low), __float_as_uint(high), 0x5410);
 }
 
 template <typename T, int D, int G, bool VEC>
-__global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a) {
+__global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a, int page_shift) {
   constexpr int kLanes = D / 8, NG = D / G;
-  const int head = blockIdx.x % a.hkv;
-  const int64_t tok = (int64_t)(blockIdx.x / a.hkv) * (kThreads / kLanes) + threadIdx.x / kLanes;
+  const uint32_t head = blockIdx.x % (uint32_t)a.hkv;
+  const int tok = blockIdx.x / (uint32_t)a.hkv * (kThreads / kLanes) + threadIdx.x / kLanes;
   const int w = threadIdx.x % kLanes;  // this thread's word of 8 coordinates
   const bool in = tok < a.n;
-  const int64_t t = in ? tok : a.n - 1;  // all lanes take part in the shuffles
+  const int t = in ? tok : (int)a.n - 1;  // all lanes take part in the shuffles
   float kx[8], vx[8];
   load8<T, VEC>(static_cast<const T*>(a.k) + t * a.k_tok + head * a.k_head + 8 * w, kx);
   load8<T, VEC>(static_cast<const T*>(a.v) + t * a.v_tok + head * a.v_head + 8 * w, vx);
-  const int64_t slot = a.slots[t];
-  const int64_t dense = (t * a.hkv + head) * D + 8 * w;
+  const int slot = __ldg(a.slots + t);
+  const int64_t dense = ((int64_t)t * a.hkv + head) * D + 8 * w;
   uint32_t ksz, vsz;
   const uint32_t kc = quantise<T, G>(kx, ksz, in && a.k_values ? static_cast<T*>(a.k_values) + dense : nullptr);
   const uint32_t vc = quantise<T, G>(vx, vsz, in && a.v_values ? static_cast<T*>(a.v_values) + dense : nullptr);
-  if (!in || slot < 0 || slot >= a.n_blocks * a.page) return;
-  const int64_t block = slot / a.page;
-  const int at = (int)(slot % a.page), ut = at % kUnit, row = key_row(ut);
-  uint8_t* unit = a.cache + ((block * a.hkv + head) * (a.page / kUnit) + at / kUnit) * (int64_t)unit_bytes(D, G);
+  if (!in || slot < 0 || (slot >> page_shift) >= a.n_blocks) return;
+  const int ut = slot % kUnit, row = key_row(ut);
+  const int64_t page = (int64_t)(slot >> page_shift) * a.hkv + head;
+  uint8_t* unit = a.cache + ((page << (page_shift - 4)) + ((slot & (a.page - 1)) >> 4)) * unit_bytes(D, G);
   reinterpret_cast<uint32_t*>(unit)[row * (D / 8) + key_word(w, D)] = kc;
   reinterpret_cast<uint32_t*>(unit + off_v(D))[ut * (D / 8) + value_word(w, ut, D)] = vc;
   if (w % (G / 8) == 0) {
@@ -130,13 +138,15 @@ cudaError_t launch(const WriteArgs& a, cudaStream_t st) {
   const int64_t per = kThreads / (D / 8);
   const int64_t blocks = (a.n + per - 1) / per * a.hkv;
   if (blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  int shift = 4;
+  while ((1 << shift) < a.page) ++shift;
   const auto fits = [](const void* p, int64_t s0, int64_t s1) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && s0 * (int64_t)sizeof(T) % 16 == 0 && s1 * (int64_t)sizeof(T) % 16 == 0;
   };
   if (fits(a.k, a.k_tok, a.k_head) && fits(a.v, a.v_tok, a.v_head))
-    write_kernel<T, D, G, true><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    write_kernel<T, D, G, true><<<(unsigned)blocks, kThreads, 0, st>>>(a, shift);
   else
-    write_kernel<T, D, G, false><<<(unsigned)blocks, kThreads, 0, st>>>(a);
+    write_kernel<T, D, G, false><<<(unsigned)blocks, kThreads, 0, st>>>(a, shift);
   return cudaGetLastError();
 }
 
