@@ -490,12 +490,14 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
         free_count_out = free_count
     else:
         _int32("free_count_out", free_count_out, (1,))
+    # the outputs in one allocation
     if lens_out is None:
-        lens_out = lens.new_empty((B,))
+        slots, cu_new, lens_out, refused = lens.new_empty((n_slots + 2 * B + 2,)).split_with_sizes(
+            (n_slots, B + 1, B, 1))
     else:
         _int32("lens_out", lens_out, (B,))
-    # cu_new, refused and slots in one allocation
-    cu_new, refused, slots = lens.new_empty((B + 2 + n_slots,)).split((B + 1, 1, n_slots))
+        slots, cu_new, refused = lens.new_empty((n_slots + B + 2,)).split_with_sizes(
+            (n_slots, B + 1, 1))
     st = lib().fq_page_step(lens.data_ptr(), new_lens.data_ptr(), B, block_tables.data_ptr(),
                             max_blocks, page, free_list.data_ptr(), n_blocks,
                             free_count.data_ptr(), lens_out.data_ptr(),

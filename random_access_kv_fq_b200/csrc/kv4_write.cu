@@ -9,8 +9,9 @@
 // kv head).  One thread takes 8 coordinates (a 16-byte load and one 32-bit word of codes) of a
 // token's key and of its value; a block takes the same kv head of 2048 / d consecutive tokens, whose
 // rows share units: their 4-byte stores join to whole sectors in L2.  What it computes is kept to
-// about 13 instructions per element, or it would be bound by their issue: rounding and clamping on
-// floats (adding 1.5 2^23 rounds to the nearest even integer), codes joined by exact FMAs.
+// about 20 instructions per element, or it would be bound by their issue: rounding on floats (adding
+// 1.5 2^23 rounds to the nearest even integer), no clamping where a group's two ends round to 0 and
+// 15 by themselves, codes joined by exact FMAs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -63,8 +64,9 @@ __device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float a, float b) {
 // and, in `sz`, the group's s (low half) and z.
 template <typename T, int G>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, T* values) {
-  float lo = fminf(fminf(fminf(x[0], x[1]), fminf(x[2], x[3])), fminf(fminf(x[4], x[5]), fminf(x[6], x[7])));
-  float hi = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+  // three at a time: one instruction each
+  float lo = fminf(fminf(fminf(fminf(x[0], x[1]), x[2]), fminf(fminf(x[3], x[4]), x[5])), fminf(x[6], x[7]));
+  float hi = fmaxf(fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), fmaxf(fmaxf(x[3], x[4]), x[5])), fmaxf(x[6], x[7]));
 #pragma unroll
   for (int m = 1; m < G / 8; m <<= 1) {
     lo = fminf(lo, __shfl_xor_sync(~0u, lo, m));
@@ -79,8 +81,14 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, 
   const float magic = 12582912.f;  // 1.5 2^23: what is added to it is rounded to an integer
   float c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    c[i] = __fadd_rn(__fadd_rn(fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], z), inv), 0.f), 15.f), magic), -magic);
+  for (int i = 0; i < 8; ++i) c[i] = __fmul_rn(__fsub_rn(x[i], z), inv);
+  // the roundings of z and s seldom move a group's ends past half a step
+  if (!((lo - z) * inv >= -0.5f && (hi - z) * inv < 15.5f)) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(c[i], 0.f), 15.f);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __fadd_rn(__fadd_rn(c[i], magic), -magic);
   if (values) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -103,7 +111,7 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, 
 }
 
 template <typename T, int D, int G, bool VEC>
-__global__ void __launch_bounds__(kThreads) write_kernel(WriteArgs a, int page_shift) {
+__global__ void __launch_bounds__(kThreads, 6) write_kernel(WriteArgs a, int page_shift) {
   constexpr int kLanes = D / 8, NG = D / G;
   const uint32_t head = blockIdx.x % (uint32_t)a.hkv;
   const int tok = blockIdx.x / (uint32_t)a.hkv * (kThreads / kLanes) + threadIdx.x / kLanes;
