@@ -71,7 +71,7 @@ _SIGS = {
                           _vp]),
     "fq_kv4_write": (_i, [_vp, _vp, _i, _c_i64, _i, _i, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp,
                           _c_i64, _i, _i, _vp, _vp, _vp]),
-    "fq_kv4_attn_workspace_bytes": (_sz, [_i]),
+    "fq_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "fq_kv4_attn": (_i, [_vp, _i, _c_i64, _i, _i, _c_i64, _c_i64, _vp, _i, _i, _vp, _c_i64, _i, _i,
                          _i, _vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
@@ -383,7 +383,7 @@ def fq_build_search_index(codebook, d: int, k: int, N: int, kind: int, L: int,
 # These calls take microseconds of GPU time, so the checks below are kept to cheap attribute reads.
 
 _KV4_UNITS = {}   # (d, group) -> unit bytes
-_KV4_WS = {}      # d -> workspace bytes
+_KV4_WS = {}      # (Hq, Hkv, d, max_q) -> workspace bytes
 
 
 def _device_index(*tensors) -> int:
@@ -457,8 +457,8 @@ def fq_kv4_unit_bytes(d: int, group: int) -> int:
     return int(lib().fq_kv4_unit_bytes(d, group))
 
 
-def fq_kv4_attn_workspace_bytes(d: int) -> int:
-    return int(lib().fq_kv4_attn_workspace_bytes(d))
+def fq_kv4_attn_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int) -> int:
+    return int(lib().fq_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q))
 
 
 def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int, n_slots: int,
@@ -579,9 +579,10 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: i
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out: a contiguous tensor of q's shape and type")
     if workspace is None:
-        ws_bytes = _KV4_WS.get(d)
+        ws_bytes = _KV4_WS.get((hq, hkv, d, max_q))
         if ws_bytes is None:
-            ws_bytes = _KV4_WS[d] = fq_kv4_attn_workspace_bytes(d)
+            ws_bytes = fq_kv4_attn_workspace_bytes(hq, hkv, d, max_q)
+            _KV4_WS[hq, hkv, d, max_q] = ws_bytes
         workspace = cache.new_empty((ws_bytes,))
     else:
         ws_bytes = workspace.numel() * workspace.element_size()

@@ -378,7 +378,7 @@ fq_status fq_wait_status(unsigned* timed_out, int clear) {
                                                wait_timeouts_encode_grid,
                                                wait_timeouts_decode, wait_timeouts_decode_large,
                                                wait_timeouts_attn, wait_timeouts_selftest,
-                                               kv4::wait_timeouts_kv4};
+                                               kv4::wait_timeouts_kv4, kv4::wait_timeouts_kv4_rows};
   for (auto rd : readers)
     if (rd(clear != 0, &n) != cudaSuccess) return FQ_ERR_CUDA;
   if (timed_out) *timed_out = n;

@@ -92,8 +92,14 @@ struct PageArgs {
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st);
-size_t attn_workspace_bytes(int d);
+size_t attn_workspace_bytes(int d, int64_t rows);  // rows: query tokens x query heads of a kv head, at most
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);  // many rows of a kv head
+size_t attn_rows_workspace_bytes(int d);
 cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_internal.h
+cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count);
+
+// Rows of a kv head up to which the register-fed kernel is the faster one.
+constexpr int64_t kFewRows = 16;
 
 }  // namespace kv4
 }  // namespace fq

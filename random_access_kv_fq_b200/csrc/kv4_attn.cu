@@ -22,12 +22,8 @@
 #include <atomic>
 #include <cfloat>
 
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include "fq_internal.h"
-#include "kv4.h"
-#include "sm100_ptx.cuh"
+#include "kv4_attn.cuh"
 
 namespace fq {
 namespace kv4 {
@@ -35,7 +31,6 @@ namespace {
 
 __device__ unsigned int g_kv4_wait_timeouts = 0;  // blocks whose bounded waits gave up
 
-constexpr int kCtas = 148;       // one block per SM
 constexpr int kChunk = 2;        // units of a stage of a warp's ring: one wait for 32 tokens
 constexpr int kItemUnits = 3;    // an item's fixed cost, in units (its queries and its end)
 
@@ -46,12 +41,6 @@ constexpr int kWarpsOf = NT == 1 ? 16 : D == 64 ? 12 : 8;
 template <int D>
 constexpr int kStagesOf = D == 64 ? 4 : 2;
 
-// What a block leaves for the second kernel: [kCtas][2] parts, part 0 of an item begun before the
-// block's range, part 1 of an item begun in it that goes on behind it.
-struct PartHeader {
-  int state;             // 0: none, 1: goes on, 3: the item's last part
-  int q0, rows, head, rb;  // where its rows are
-};
 template <int NT, int D>
 struct Part {
   float4 o[NT * D / 16 * 32];  // accumulators in fragment order
@@ -59,40 +48,6 @@ struct Part {
 };
 
 // ------------------------------------------------------------------------------ items
-
-struct Seq {
-  int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
-  int cost;                    // of each of its row blocks, in units: the most that one may see
-};
-
-template <int NB>
-__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
-  Seq s;
-  s.n = min(max(__ldg(a.kv_lens + b), 0), a.max_blocks * a.page);
-  s.q0 = b;
-  s.m = 1;
-  if (a.cu_q) {
-    s.q0 = __ldg(a.cu_q + b);
-    s.m = max(0, min(__ldg(a.cu_q + b + 1) - s.q0, a.max_q));
-    if (s.q0 < 0 || s.q0 > a.n_q - s.m) s.m = 0;
-  }
-  s.rows = s.m * r;
-  s.blocks = (s.rows + NB - 1) / NB;
-  s.cost = s.n;
-  if (a.window > 0) s.cost = min(s.n, min(a.window, 1 << 30) + NB + kUnit);
-  s.cost = (s.cost + kUnit - 1) / kUnit + kItemUnits;
-  return s;
-}
-
-// (x & mask) | bits in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
-  uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
-  return y;
-}
-
-__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
-__device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
 
 __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                       uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -123,39 +78,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-template <int BYTES>
-__device__ __forceinline__ void lds(uint32_t at, uint32_t* x) {
-  if constexpr (BYTES == 16)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
-  else if constexpr (BYTES == 8)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at));
-  else
-    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[0]) : "r"(at));
-}
-
 // ------------------------------------------------------------------------------ one warp's state
-
-template <typename T>
-__device__ __forceinline__ float q_float(uint16_t x) {
-  if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) return __uint_as_float((uint32_t)x << 16);
-  else return __half2float(__ushort_as_half(x));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t pack_out(float a, float b) {
-  if constexpr (__is_same(T, __half)) {
-    return u32(__floats2half2_rn(a, b));
-  } else {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
 
 template <typename T, int D, int G, int NT>
 struct Warp {
@@ -564,7 +487,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     block = blockIdx.x % own_blocks;
     head = blockIdx.x / own_blocks % a.hkv;
     b = blockIdx.x / own_blocks / a.hkv;
-    s = load_seq<NB>(a, b, r);
+    s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
     if (block < s.blocks) {
       s.cost = kItemUnits + W;  // a W-th of the units each, whatever their number
       from = warp == 0 ? 0 : kItemUnits + warp;
@@ -576,7 +499,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     const int per = (a.B + 32 * W - 1) / (32 * W), b0 = tid * per, b1 = min(a.B, b0 + per);
     int64_t mine = 0;
     for (int i = b0; i < b1; ++i) {
-      s = load_seq<NB>(a, i, r);
+      s = load_seq<NB, kUnit, kItemUnits>(a, i, r);
       mine += (int64_t)(a.hkv * s.blocks) * s.cost;
     }
     int64_t x = mine;
@@ -598,7 +521,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     if (below + mine > block0 && below < block0 + W * span) {
       for (int i = b0; i < b1; ++i) {
         if (per > 1) {
-          s = load_seq<NB>(a, i, r);
+          s = load_seq<NB, kUnit, kItemUnits>(a, i, r);
           mine = (int64_t)(a.hkv * s.blocks) * s.cost;
         }
 #pragma unroll 1
@@ -616,7 +539,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     left = min(span, total - block0 - warp * span);
     if (left > 0) {
       b = start_b[warp];
-      s = load_seq<NB>(a, b, r);
+      s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
       const int64_t in_seq = start_in[warp];
       // which of the sequence's items, all of one cost; the estimate is off by one at most
       int64_t item = (int64_t)((double)in_seq / s.cost);
@@ -741,7 +664,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       block = 0;
       if (++head == a.hkv) {
         head = 0;
-        do s = load_seq<NB>(a, ++b, r); while (s.blocks == 0);
+        do s = load_seq<NB, kUnit, kItemUnits>(a, ++b, r); while (s.blocks == 0);
       }
     }
   }
@@ -808,17 +731,10 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const PartHeader* hdr = static_cast<const PartHeader*>(a.workspace);
   const P* part = reinterpret_cast<const P*>(static_cast<const uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const int c0 = blockIdx.x;
   const PartHeader h = hdr[c0 * 2 + 1];
   if (h.state != 1) return;
-  int end = kCtas - 1;  // the block that holds the item's last part
-  for (int c = c0 + 1; c < kCtas; c += 32) {
-    const uint32_t last = __ballot_sync(~0u, c + lane < kCtas && hdr[(c + lane) * 2].state == 3);
-    if (last) {
-      end = c + __ffs(last) - 1;
-      break;
-    }
-  }
+  const int end = last_part(hdr, c0);
   for (int e = threadIdx.x; e < NT * D / 16 * 32; e += blockDim.x) {
     const int row = ((e >> 5) / (D / 16)) * 8 + 2 * (e & 3);
     Join join;
@@ -851,8 +767,7 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   constexpr size_t ring = kStagesOf<D> * kChunk * unit_bytes(D, G), slot = ring > sizeof(P) ? ring : sizeof(P);
   constexpr size_t bytes = W * (slot + sizeof(P));
   static_assert(bytes + 2048 <= 227 * 1024, "shared memory of a block, static included");
-  static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0 && 2 * kCtas * sizeof(PartHeader) % 16 == 0,
-                "parts are read in 16 bytes");
+  static_assert(slot % 16 == 0 && sizeof(P) % 16 == 0, "parts are read in 16 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -901,11 +816,13 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int d) {
+size_t attn_workspace_bytes(int d, int64_t rows) {
+  if (rows > kFewRows) return attn_rows_workspace_bytes(d);
   return 2 * kCtas * (sizeof(PartHeader) + (d == 64 ? sizeof(Part<2, 64>) : sizeof(Part<2, 128>)));
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {
+  if ((int64_t)a.max_q * (a.hq / a.hkv) > kFewRows) return launch_attn_rows(a, st);
   return a.type == FQ_F16 ? launch_shape<__half>(a, st) : launch_shape<__nv_bfloat16>(a, st);
 }
 

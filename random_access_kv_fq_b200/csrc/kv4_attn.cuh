@@ -1,0 +1,103 @@
+// What the two attention kernels over the 4-bit cache share: how items are cut, how q is read and
+// out written, small wrappers.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kv4.h"
+#include "sm100_ptx.cuh"
+
+namespace fq {
+namespace kv4 {
+
+constexpr int kCtas = 148;  // one block per SM
+
+// What a block leaves for the kernel that joins: [kCtas][2] parts, part 0 of an item begun before the
+// block's range, part 1 of an item begun in it that goes on behind it.
+struct PartHeader {
+  int state;             // 0: none, 1: goes on, 3: the item's last part
+  int q0, rows, head, rb;  // where its rows are
+};
+static_assert(2 * kCtas * sizeof(PartHeader) % 16 == 0, "parts behind the headers are read in 16 bytes");
+
+// The block that holds the last part of the item begun in block c0.  All lanes of a warp call it.
+__device__ __forceinline__ int last_part(const PartHeader* hdr, int c0) {
+  const int lane = threadIdx.x & 31;
+  for (int c = c0 + 1; c < kCtas; c += 32) {
+    const uint32_t last = __ballot_sync(~0u, c + lane < kCtas && hdr[(c + lane) * 2].state == 3);
+    if (last) return c + __ffs(last) - 1;
+  }
+  return kCtas - 1;
+}
+
+struct Seq {
+  int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
+  int cost;                    // of each of its row blocks: the most that one may see
+};
+
+// Row blocks of NB rows; their cost is in steps of STEP tokens, FIXED of them for each row block's
+// queries and its end.
+template <int NB, int STEP, int FIXED>
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
+  Seq s;
+  s.n = min(max(__ldg(a.kv_lens + b), 0), a.max_blocks * a.page);
+  s.q0 = b;
+  s.m = 1;
+  if (a.cu_q) {
+    s.q0 = __ldg(a.cu_q + b);
+    s.m = max(0, min(__ldg(a.cu_q + b + 1) - s.q0, a.max_q));
+    if (s.q0 < 0 || s.q0 > a.n_q - s.m) s.m = 0;
+  }
+  s.rows = s.m * r;
+  s.blocks = (s.rows + NB - 1) / NB;
+  s.cost = s.n;
+  if (a.window > 0) s.cost = min(s.n, min(a.window, 1 << 30) + NB + kUnit);
+  s.cost = (s.cost + STEP - 1) / STEP + FIXED;
+  return s;
+}
+
+// (x & mask) | bits in one instruction
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+  uint32_t y;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  return y;
+}
+
+__device__ __forceinline__ __half2 h2(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
+__device__ __forceinline__ uint32_t u32(__half2 x) { return *reinterpret_cast<uint32_t*>(&x); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void lds(uint32_t at, uint32_t* x) {
+  if constexpr (BYTES == 16)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at));
+  else if constexpr (BYTES == 8)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x[0]), "=r"(x[1]) : "r"(at));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x[0]) : "r"(at));
+}
+
+template <typename T>
+__device__ __forceinline__ float q_float(uint16_t x) {
+  if constexpr (sizeof(T) == 2 && !__is_same(T, __half)) return __uint_as_float((uint32_t)x << 16);
+  else return __half2float(__ushort_as_half(x));
+}
+template <typename T>
+__device__ __forceinline__ uint32_t pack_out(float a, float b) {
+  if constexpr (__is_same(T, __half)) {
+    return u32(__floats2half2_rn(a, b));
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+}  // namespace kv4
+}  // namespace fq

@@ -1,0 +1,726 @@
+// Attention over the 4-bit paged cache for many rows of a kv head (chunks of a prompt, drafted
+// tokens): 128 rows (query token, query head) at a time on the fifth-generation tensor cores.
+//
+// One block per SM, its warps in roles that meet in mbarriers:
+//   loader   copies units (bulk copies) into a ring of 64-token tiles of packed cache;
+//   unpack   4 warps turn a tile into fp16 operands in shared memory, two tiles deep;
+//   mma      one thread issues tcgen05.mma: S = Q K^T into one of two buffers of tensor memory,
+//            O += P V with P in tensor memory, the next tile's S under this tile's softmax;
+//   softmax  4 warps, a thread to a row: S out of tensor memory, weights P back into it.
+// With codes c, steps s and zeros z, scores carry no 16-bit rounding of the keys: s is split into its
+// leading 7 bits and the rest, so that s_hi c and s_lo c are fp16 numbers exactly, and
+//   S = Q (s_hi C)^T + Q (s_lo C)^T + qsum Z^T,
+// the last one a 16-wide product of the groups' sums of q (in two parts) with the zeros.  Values are
+// fp16(c s + z); weights are fp16, for fp16 outputs in two parts.  q is scaled to fp16 by a power of
+// two per row.  The softmax runs to base 2 against a maximum that moves only when a score passes it
+// by 8; moving it rescales O in tensor memory.
+//
+// Per 64 tokens and 128 rows of d = 128 the tensor pipe needs about 800 cycles (1,056 with weights in
+// two parts), the softmax about 500 instructions of each of its warps.
+#include <atomic>
+#include <cfloat>
+
+#include "fq_internal.h"
+#include "kv4_attn.cuh"
+
+namespace fq {
+namespace kv4 {
+namespace {
+
+__device__ unsigned int g_kv4_rows_wait_timeouts = 0;  // blocks whose bounded waits gave up
+
+constexpr int kRows = 128;      // rows of a block's item
+constexpr int kTile = 64;       // tokens of a tile
+constexpr int kTileUnits = kTile / kUnit;
+constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
+constexpr int kRing = 3;        // packed tiles in flight
+constexpr int kUnpackWarps = 4;
+constexpr int kWarps = 4 + kUnpackWarps + 2;  // softmax (which own tensor memory lanes), unpack, mma, loader
+
+template <int D>
+struct RowsPart {
+  float o[kRows][D];
+  float m[kRows], l[kRows];
+};
+
+template <int D, int G>
+struct Shape {
+  static constexpr int NG = D / G, UB = unit_bytes(D, G), KB = D / 32, NA = D / 64;
+  static constexpr int kK = kTile * D * 2;           // bytes of one fp16 operand of a tile
+  static constexpr int kZ = kTile * 32;              // zeros: 16 numbers a token
+  static constexpr int kBuf = 3 * kK + kZ;           // s_hi C, s_lo C, V, Z
+  static constexpr int kPacked = kTileUnits * UB;
+  static constexpr size_t kSmem = 1024 + 2 * kBuf + kRing * kPacked;
+  // tensor memory columns
+  static constexpr uint32_t S = 0, O = 128, Q = O + D, QZ = Q + D / 2, P = 352;  // P: [2][hi, lo][32]
+  static_assert(QZ + 8 <= P && P + 128 <= 512, "tensor memory");
+};
+
+struct Control {
+  uint64_t ring_full[kRing], ring_empty[kRing];
+  uint64_t kv_full[2], pv_done[2], s_full[2], p_full[2], q_full;
+  uint32_t tmem;
+  int gave_up;
+  int gone[8];  // units of the last eight tiles that are not there (bits)
+  int64_t sums[kWarps];
+  int start_b;
+  int64_t start_in;
+};
+
+// A bounded wait that all of the block gives up together.
+__device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
+  for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
+    if (ptx::mbar_try(bar, parity & 1)) return true;
+    if ((i & 63) == 63 && *(volatile int*)&c->gave_up) return false;
+  }
+  *(volatile int*)&c->gave_up = 1;
+  return false;
+}
+
+// The items of a block's range of the line, one at a time, the same in every role.
+template <int D>
+struct Items {
+  int64_t left;
+  int from, b, head, block;
+  Seq s;
+  // of the current item
+  int to, rb, end, first, base_u, t0, t1, past;
+  __device__ __forceinline__ bool next(const AttnArgs& a, int r, bool begun) {
+    if (begun) {
+      from = 0;
+      if (left > 0 && ++block == s.blocks) {
+        block = 0;
+        if (++head == a.hkv) {
+          head = 0;
+          do s = load_seq<kRows, kTile, kItemTiles>(a, ++b, r); while (s.blocks == 0);
+        }
+      }
+    }
+    if (left <= 0) return false;
+    to = (int)min((int64_t)s.cost, from + left);
+    left -= to - from;
+    // row blocks from both ends in turn: two neighbours see about as many tokens as any two
+    rb = block & 1 ? s.blocks - 1 - (block >> 1) : block >> 1;
+    past = s.n - s.m + 1;
+    const uint32_t row0 = rb * kRows, row1 = min(rb * kRows + kRows, s.rows) - 1;
+    end = max(0, past + (int)(row1 / (uint32_t)r));
+    first = a.window > 0 ? max(0, past + (int)(row0 / (uint32_t)r) - a.window) : 0;
+    base_u = first / kUnit;
+    const int tiles = end > first ? (end - base_u * kUnit + kTile - 1) / kTile : 0;
+    const int full = s.cost - kItemTiles;
+    const float ratio = (float)tiles / (float)full;
+    const auto share = [&](int x) {
+      x -= kItemTiles;
+      return x <= 0 ? 0 : x >= full ? tiles : tiles == full ? x : min(tiles, (int)(x * ratio));
+    };
+    t0 = share(from);
+    t1 = share(to);
+    return true;
+  }
+};
+
+// ------------------------------------------------------------------------------ unpacking
+
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// The 8 codes of a word as exact fp16 numbers, in the order 0 4 | 1 5 | 2 6 | 3 7.
+__device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) {
+  const __half2 bias = h2(0xE400E400u), sixteenth = h2(0x2C002C00u), bias16 = h2(0xD400D400u);
+  const uint32_t w8 = w >> 8;
+  c[0] = __hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), bias);
+  c[1] = __hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+  c[2] = __hadd2(h2(and_or(w8, 0x000F000Fu, 0x64006400u)), bias);
+  c[3] = __hfma2(h2(and_or(w8, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+}
+
+// This warp's share of a tile: steps of 32 lanes, each a 16-byte chunk (4 words) of a token's keys
+// or values.  K rows go K-major, V rows MN-major, both with the 128-byte swizzle; lanes are spread
+// so that no eight of them meet in a bank.
+template <int D, int G>
+__device__ __forceinline__ void unpack_tile(uint32_t packed, uint32_t buf, int warp, int lane, int pos0, int first, int end, int gone) {
+  using C = Shape<D, G>;
+  constexpr int kChunks = D / 32, kTokens = 32 / kChunks, kSteps = kTile / kTokens;
+#pragma unroll 1
+  for (int i = warp; i < kSteps; i += kUnpackWarps) {
+    const int ch = lane % kChunks, row = i * kTokens + lane / kChunks;  // row: place in the tile's packed order
+    const int unit = row / kUnit, place = row % kUnit;
+    const uint32_t u = packed + unit * C::UB;
+    uint32_t w[4], sc[C::NG];
+    // keys: packed row `place` holds token 0 4 1 5 2 6 3 7 (+ 8)
+    lds<16>(u + place * (D / 2) + ch * 16, w);
+    lds<4 * C::NG>(u + off_ks(D) + place * 4 * C::NG, sc);
+    const int tok = (place >> 1 & 3) + 4 * (place & 1) + (place & 8), n = unit * kUnit + tok;
+    const uint32_t krow = buf + n * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int kb = j % C::KB, t = D == 128 ? ch : 2 * ch + (j >> 1), word = 4 * kb + t;
+      const int g = 32 * kb / G;
+      const uint32_t s = C::NG == 1 ? sc[0] & 0xFFFFu : (sc[g / 2] >> (16 * (g & 1))) & 0xFFFFu;
+      const uint32_t shi = s & 0xFFF0u;
+      const __half2 s_hi = h2(shi | shi << 16), s_all = h2(s | s << 16), s_lo = __hsub2(s_all, s_hi);
+      __half2 c[4];
+      codes(w[j], c);
+      const uint32_t at = krow + (word >> 3) * (kTile * 128) + (((word & 7) ^ (n & 7)) << 4);
+      sts16(at, u32(__hmul2(c[0], s_hi)), u32(__hmul2(c[1], s_hi)), u32(__hmul2(c[2], s_hi)), u32(__hmul2(c[3], s_hi)));
+      sts16(at + C::kK, u32(__hmul2(c[0], s_lo)), u32(__hmul2(c[1], s_lo)), u32(__hmul2(c[2], s_lo)), u32(__hmul2(c[3], s_lo)));
+    }
+    if (ch == 0) {
+      // zeros twice (for the two parts of the sums of q), then nothing
+      const uint32_t at = buf + 3 * C::kK + ptx::noswz16_offset(n, 0);
+      if constexpr (C::NG == 4) sts16(at, sc[2], sc[3], sc[2], sc[3]);
+      else if constexpr (C::NG == 2) sts16(at, sc[1], sc[1], 0, 0);
+      else sts16(at, __byte_perm(sc[0], 0, 0x3232), 0, 0, 0);
+    }
+    // values: packed row = token
+    uint32_t sz = 0;
+    lds<16>(u + off_v(D) + place * (D / 2) + ch * 16, w);
+    const int group = D == 128 ? ch ^ (place & 2) : ch;  // 32 coordinates
+    lds<4>(u + off_vs(D, G) + (place * C::NG + group * 32 / G) * 4, &sz);
+    const int pos = pos0 + row;
+    if (pos < first || pos >= end || (gone >> unit & 1)) sz = 0;  // nobody sees it: its value becomes 0
+    if (D == 128 && (group & 2)) {
+      uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
+      x = w[1]; w[1] = w[3]; w[3] = x;
+    }
+    const __half2 st = h2(__byte_perm(sz, 0, 0x1010)), ze = h2(__byte_perm(sz, 0, 0x3232));
+    const uint32_t vrow = buf + 2 * C::kK + (row >> 3) * (C::NA * 1024) + (row & 7) * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int word = 4 * group + (D == 128 ? j ^ (group & 2) : j);
+      __half2 c[4];
+      codes(w[j], c);
+      sts16(vrow + (word >> 3) * 1024 + (((word & 7) ^ (row & 7)) << 4), u32(__hfma2(c[0], st, ze)), u32(__hfma2(c[1], st, ze)),
+            u32(__hfma2(c[2], st, ze)), u32(__hfma2(c[3], st, ze)));
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ the kernel
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int page_shift) {
+  using C = Shape<D, G>;
+  constexpr bool kTwoParts = __is_same(T, __half);
+  extern __shared__ uint8_t raw_smem[];
+  __shared__ Control ctl;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+  uint8_t* packed = smem + 2 * C::kBuf;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r = a.hq / a.hkv;
+
+  if (tid == 0) {
+    ctl.gave_up = 0;
+    for (int i = 0; i < kRing; ++i) {
+      ptx::mbar_init(&ctl.ring_full[i], kTileUnits);
+      ptx::mbar_init(&ctl.ring_empty[i], kUnpackWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&ctl.kv_full[i], kUnpackWarps);
+      ptx::mbar_init(&ctl.pv_done[i], 1);
+      ptx::mbar_init(&ctl.s_full[i], 1);
+      ptx::mbar_init(&ctl.p_full[i], 4);
+    }
+    ptx::mbar_init(&ctl.q_full, 4);
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0) {
+    ptx::tmem_alloc(&ctl.tmem, 512);
+    ptx::tmem_relinquish();
+  }
+  // the upper half of the zeros' 16 numbers is never written again
+  for (int i = tid; i < 2 * kTile; i += 32 * kWarps)
+    sts16(ptx::smem_u32(smem) + (i / kTile) * C::kBuf + 3 * C::kK + ptx::noswz16_offset(i % kTile, 8), 0, 0, 0, 0);
+  ptx::fence_proxy_async_smem();
+
+  // The line of all items' costs, cut into one range per block; the thread whose sequences hold the
+  // range's start tells the block.
+  Items<D> it;
+  {
+    const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = tid * per, b1 = min(a.B, b0 + per);
+    int64_t mine = 0;
+    for (int i = b0; i < b1; ++i) {
+      it.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+      mine += (int64_t)(a.hkv * it.s.blocks) * it.s.cost;
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 31) ctl.sums[warp] = x;
+    __syncthreads();
+    int64_t below = x - mine, total = 0;
+#pragma unroll 1
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) below += ctl.sums[w];
+      total += ctl.sums[w];
+    }
+    const int64_t span = max((int64_t)(total * (1.0 / kCtas)) + 1, (int64_t)kItemTiles + 2);
+    const int64_t x0 = blockIdx.x * span;
+    for (int i = b0; i < b1 && below <= x0; ++i) {
+      if (per > 1) {
+        it.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+        mine = (int64_t)(a.hkv * it.s.blocks) * it.s.cost;
+      }
+      if (x0 < below + mine) {
+        ctl.start_b = i;
+        ctl.start_in = x0 - below;
+      }
+      below += mine;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    it.left = min(span, total - x0);
+    it.from = it.b = it.head = it.block = 0;
+    if (it.left > 0) {
+      it.b = ctl.start_b;
+      it.s = load_seq<kRows, kTile, kItemTiles>(a, it.b, r);
+      // which of the sequence's items, all of one cost; the estimate is off by one at most
+      int64_t item = (int64_t)((double)ctl.start_in / it.s.cost);
+      if (item * it.s.cost > ctl.start_in) --item;
+      if (ctl.start_in - item * it.s.cost >= it.s.cost) ++item;
+      it.from = (int)(ctl.start_in - item * it.s.cost);
+      it.head = (int)item / it.s.blocks;
+      it.block = (int)item - it.head * it.s.blocks;
+    }
+  }
+  const uint32_t tmem = ctl.tmem;
+  const uint32_t smem32 = ptx::smem_u32(smem), packed32 = smem32 + 2 * C::kBuf;
+  uint32_t tile = 0;  // tiles so far, over all items: buffers and parities
+  PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
+
+  if (warp < 4) {
+    // ---------------------------------------------------------------- softmax
+    RowsPart<D>* out_part = reinterpret_cast<RowsPart<D>*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
+    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    int left_part[2] = {0, 0};
+    bool ok = true;
+    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+      const uint32_t row = it.rb * kRows + tid;
+      const bool in = row < (uint32_t)it.s.rows;
+      const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
+      float m = -FLT_MAX, l = 0.f, kappa = 0.f;
+      const uint32_t last_row = min(it.rb * kRows + kRows, it.s.rows) - 1;
+      const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? hi - a.window : 0;
+      if (it.t0 < it.t1) {
+        // this thread's row of q, by a power of two in fp16, its keys' order of coordinates
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(it.s.q0 + tok) * a.q_tok + (int64_t)(it.head * r + hh) * a.q_head;
+        const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0;
+        auto word = [&](int w) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (!in) return v;
+          const uint16_t* p = src + 8 * w;
+          if (wide) return __ldg(reinterpret_cast<const uint4*>(p));
+          v.x = __ldg(p) | (uint32_t)__ldg(p + 1) << 16;
+          v.y = __ldg(p + 2) | (uint32_t)__ldg(p + 3) << 16;
+          v.z = __ldg(p + 4) | (uint32_t)__ldg(p + 5) << 16;
+          v.w = __ldg(p + 6) | (uint32_t)__ldg(p + 7) << 16;
+          return v;
+        };
+        float top = 0.f;
+#pragma unroll 4
+        for (int w = 0; w < D / 8; ++w) {
+          const uint4 v = word(w);
+          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            top = fmaxf(top, fmaxf(fabsf(q_float<T>((uint16_t)x[i])), fabsf(q_float<T>((uint16_t)(x[i] >> 16)))));
+        }
+        const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 134, -126) : 0;
+        float down = __uint_as_float((uint32_t)(127 - e) << 23);
+        kappa = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
+        if (kappa < 0.f) {  // the largest score is the largest product
+          kappa = -kappa;
+          down = -down;
+        }
+        kappa = fmaxf(kappa, 1e-37f);  // so that -inf, a masked score, stays that
+        float sum[C::NG];
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
+#pragma unroll
+        for (int w4 = 0; w4 < D / 8; w4 += 4) {  // 32 coordinates: 16 columns
+          uint32_t col[16];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint4 v = word(w4 + i);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            __half y[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              y[k] = __float2half_rn(q_float<T>((uint16_t)(x[k / 2] >> (16 * (k & 1)))) * down);
+              sum[8 * w4 / G] += __half2float(y[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) col[4 * i + k] = u32(__halves2half2(y[k], y[k + 4]));
+          }
+          __syncwarp();
+          ptx::tmem_st16(lanes + C::Q + 4 * w4, col);
+        }
+        uint32_t qz[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        __half part[2][C::NG];
+#pragma unroll
+        for (int i = 0; i < C::NG; ++i) {
+          part[0][i] = __float2half_rn(sum[i]);
+          part[1][i] = __float2half_rn(sum[i] - __half2float(part[0][i]));
+        }
+        if constexpr (C::NG == 1) {
+          qz[0] = u32(__halves2half2(part[0][0], part[1][0]));
+        } else {
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int i = 0; i < C::NG; i += 2) qz[(p * C::NG + i) / 2] = u32(__halves2half2(part[p][i], part[p][i + 1]));
+        }
+        ptx::tmem_st8(lanes + C::QZ, qz);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
+
+        for (int j = it.t0; j < it.t1; ++j, ++tile) {
+          const uint32_t buf = tile & 1;
+          ok = wait(&ctl, &ctl.s_full[buf], tile >> 1);
+          ok = __all_sync(~0u, ok);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          uint32_t sr[64];
+          ptx::tmem_ld_cols<0, 64>(lanes + C::S + 64 * buf, sr);
+          ptx::tmem_wait_ld();
+          const int pos0 = it.base_u * kUnit + j * kTile;
+          // what this row sees of the tile: columns [c0, c1), less units that are not there
+          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[tile & 7];
+          if (__any_sync(~0u, c0 > 0 || c1 < kTile || gone != 0)) {
+#pragma unroll
+            for (int c = 0; c < kTile; ++c)
+              if (c < c0 || c >= c1 || (gone >> (c / kUnit) & 1)) sr[c] = 0xFF800000u;
+          }
+          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(sr[c + i])), __uint_as_float(sr[c + 4 + i]));
+          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * kappa;
+          if (__any_sync(~0u, top > m + 8.f)) {
+            const float now = fmaxf(m, top), f = ex2(m - now);
+            m = now;
+            l *= f;
+            if (j > it.t0) {
+              // O is this warp's once the tile before is in it
+              ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1));
+              if (!ok) break;
+              ptx::tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                ptx::tmem_ld16(lanes + C::O + c, o);
+                ptx::tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                ptx::tmem_st16(lanes + C::O + c, o);
+              }
+              ptx::tmem_wait_st();
+            }
+          }
+          float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+          // P of this buffer was used two tiles ago
+          if (tile >= 2) {
+            ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[buf], (tile - 2) >> 1));
+            if (!ok) break;
+            ptx::tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < kTile; c += 32) {
+            uint32_t p[16], pl[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float s0 = __uint_as_float(sr[c + 2 * i]), s1 = __uint_as_float(sr[c + 2 * i + 1]);
+              const float x = ex2(fmaf(s0, kappa, -m)), y = ex2(fmaf(s1, kappa, -m));
+              sum4[i & 3] += x + y;
+              const __half2 v = __floats2half2_rn(x, y);
+              p[i] = u32(v);
+              if (kTwoParts) {
+                const float2 back = __half22float2(v);
+                pl[i] = u32(__floats2half2_rn(x - back.x, y - back.y));
+              }
+            }
+            ptx::tmem_st16(lanes + C::P + 64 * buf + c / 2, p);
+            if (kTwoParts) ptx::tmem_st16(lanes + C::P + 64 * buf + 32 + c / 2, pl);
+          }
+          l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl.p_full[buf]);
+        }
+        if (!ok) break;
+        ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1));
+        if (!ok) break;
+        ptx::tc_fence_after();
+      }
+      const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.s.cost;
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      const int k = it.from > 0 ? 0 : 1;
+      RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
+      T* dst = static_cast<T*>(a.out) + ((int64_t)(it.s.q0 + tok) * a.hq + it.head * r + hh) * D;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 16) {
+        uint32_t o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = 0;
+        __syncwarp();
+        if (any) {
+          ptx::tmem_ld16(lanes + C::O + c, o);
+          ptx::tmem_wait_ld();
+        }
+        if (!in) continue;
+        float v[16];  // columns are coordinates 0 4 1 5 2 6 3 7 of each eight
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[(i & 8) + (i >> 1 & 3) + 4 * (i & 1)] = __uint_as_float(o[i]);
+        if (whole) {
+#pragma unroll
+          for (int i = 0; i < 16; i += 8)
+            *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack_out<T>(v[i] * inv, v[i + 1] * inv), pack_out<T>(v[i + 2] * inv, v[i + 3] * inv),
+                                                                pack_out<T>(v[i + 4] * inv, v[i + 5] * inv), pack_out<T>(v[i + 6] * inv, v[i + 7] * inv));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&part->o[tid][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+      }
+      if (!whole) {
+        if (in) {
+          part->m[tid] = m;
+          part->l[tid] = l;
+        }
+        left_part[k] = 1;
+        if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{it.to == it.s.cost ? 3 : 1, it.s.q0, it.s.rows, it.head, it.rb};
+      }
+      ptx::tc_fence_before();  // O is read before the next item's products
+    }
+    if (tid == 0)
+      for (int k = 0; k < 2; ++k)
+        if (!left_part[k]) out_hdr[blockIdx.x * 2 + k].state = 0;
+  } else if (warp < 4 + kUnpackWarps) {
+    // ---------------------------------------------------------------- unpack
+    bool ok = true;
+    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+      for (int j = it.t0; j < it.t1; ++j, ++tile) {
+        const uint32_t slot = tile % kRing, buf = tile & 1;
+        ok = wait(&ctl, &ctl.ring_full[slot], tile / kRing);
+        if (ok && tile >= 2) ok = wait(&ctl, &ctl.pv_done[buf], (tile - 2) >> 1);
+        ok = __all_sync(~0u, ok);
+        if (!ok) break;
+        const uint32_t at = packed32 + slot * C::kPacked;
+        unpack_tile<D, G>(at, smem32 + buf * C::kBuf, warp - 4, lane, it.base_u * kUnit + j * kTile, it.first, it.end,
+                          *(volatile int*)&ctl.gone[tile & 7]);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          ptx::mbar_arrive(&ctl.kv_full[buf]);
+          ptx::mbar_arrive(&ctl.ring_empty[slot]);
+        }
+      }
+    }
+  } else if (warp == 4 + kUnpackWarps) {
+    // ---------------------------------------------------------------- mma
+    constexpr uint32_t idesc_s = ptx::idesc_f16_f32(128, kTile), idesc_o = ptx::idesc_f16_f32(128, D) | (1u << 16);
+    bool ok = true;
+    uint32_t item = 0;
+    auto scores = [&](uint32_t t) {  // S of tile t
+      const uint32_t buf = t & 1, base = smem32 + buf * C::kBuf, d = tmem + C::S + 64 * buf;
+#pragma unroll
+      for (int part = 0; part < 2; ++part)
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)
+          ptx::umma_f16_ts(d, tmem + C::Q + 8 * ks, ptx::sdesc_kmajor_sw128(base + part * C::kK + (ks >> 2) * (kTile * 128) + (ks & 3) * 32),
+                           idesc_s, part > 0 || ks > 0 ? 1u : 0u);
+      ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 3 * C::kK, 128, 256), idesc_s, 1u);
+      ptx::umma_commit(&ctl.s_full[buf]);
+    };
+    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+      if (it.t0 >= it.t1) continue;
+      if (lane == 0) {
+        ok = wait(&ctl, &ctl.q_full, item) && wait(&ctl, &ctl.kv_full[tile & 1], tile >> 1);
+        if (ok) {
+          ptx::tc_fence_after();
+          scores(tile);
+        }
+        for (int j = it.t0; j < it.t1 && ok; ++j) {
+          const uint32_t t = tile + (j - it.t0), buf = t & 1;
+          if (j + 1 < it.t1) {
+            ok = wait(&ctl, &ctl.kv_full[buf ^ 1], (t + 1) >> 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            scores(t + 1);
+          }
+          ok = wait(&ctl, &ctl.p_full[buf], t >> 1);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t v = smem32 + buf * C::kBuf + 2 * C::kK;
+#pragma unroll
+          for (int part = 0; part < (kTwoParts ? 2 : 1); ++part)
+#pragma unroll
+            for (int ks = 0; ks < kTile / 16; ++ks)
+              ptx::umma_f16_ts(tmem + C::O, tmem + C::P + 64 * buf + 32 * part + 8 * ks,
+                               ptx::sdesc_mnmajor_sw128(v + ks * 2 * C::NA * 1024, 1024, C::NA * 1024), idesc_o,
+                               j > it.t0 || part > 0 || ks > 0 ? 1u : 0u);
+          ptx::umma_commit(&ctl.pv_done[buf]);
+        }
+      }
+      ok = __shfl_sync(~0u, (int)ok, 0);
+      tile += it.t1 - it.t0;
+      ++item;
+    }
+  } else {
+    // ---------------------------------------------------------------- loader
+    bool ok = true;
+    const int shift = page_shift - 4;
+    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+      const int32_t* table = a.tables + (int64_t)it.b * a.max_blocks;
+      const int u_begin = it.base_u + it.t0 * kTileUnits, u_end = min(it.base_u + it.t1 * kTileUnits, (it.end + kUnit - 1) / kUnit);
+      auto entry = [&](int u) { return u < u_end ? __ldg(table + (u >> shift)) : -1; };
+      // lane i holds the table entry of units i, i + 32, ... of the part; the next 32 are on their way
+      int id = -1, id_next = it.t0 < it.t1 ? entry(u_begin + lane) : -1;
+      for (int j = it.t0; j < it.t1; ++j, ++tile) {
+        const int at = ((j - it.t0) * kTileUnits) & 31;
+        if (at == 0) {
+          id = id_next;
+          id_next = entry(u_begin + (j - it.t0) * kTileUnits + 32 + lane);
+        }
+        const uint32_t slot = tile % kRing;
+        if (tile >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[slot], tile / kRing - 1));
+        if (!ok) break;
+        const bool good = id >= 0 && id < a.n_blocks;
+        const uint32_t there = __ballot_sync(~0u, good) >> at;
+        // This place is free: the tile three back is unpacked, so the products of the one five back are
+        // done, and the softmax is past the one eight back.
+        if (lane == at) *(volatile int*)&ctl.gone[tile & 7] = ~there & ((1 << kTileUnits) - 1);
+        __syncwarp();
+        const int i = lane - at;
+        if ((unsigned)i < kTileUnits) {
+          if (good) {
+            const int u = u_begin + (j - it.t0) * kTileUnits + i;
+            const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
+            ptx::mbar_arrive_expect_tx(&ctl.ring_full[slot], C::UB);
+            ptx::bulk_load(packed + slot * C::kPacked + i * C::UB, src, C::UB, &ctl.ring_full[slot]);
+          } else {
+            ptx::mbar_arrive(&ctl.ring_full[slot]);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    // copies in flight land before the block ends, also where a wait gave up
+    if (!ok)
+      for (uint32_t t = tile > kRing ? tile - kRing : 0; t < tile; ++t) ptx::mbar_wait(&ctl.ring_full[t % kRing], (t / kRing) & 1);
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (ctl.gave_up && warp == 0) {
+    // products that may be in flight: the last ones were committed to these
+    for (int i = 0; i < 2; ++i)
+      for (uint32_t n = 0; n < 4096 && !ptx::mbar_try(&ctl.pv_done[i], 0) && !ptx::mbar_try(&ctl.pv_done[i], 1); ++n) {}
+    if (lane == 0) atomicAdd(&g_kv4_rows_wait_timeouts, 1u);
+  }
+  if (warp == 0) ptx::tmem_dealloc(tmem, 512);
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+
+// Joins the parts of the items that span blocks: blocks (c, i) rows 16 i .. of the item begun in block
+// c of the first kernel.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) rows_join_kernel(AttnArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const PartHeader* hdr = static_cast<const PartHeader*>(a.workspace);
+  const RowsPart<D>* part = reinterpret_cast<const RowsPart<D>*>(static_cast<const uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
+  const int c0 = blockIdx.x;
+  const PartHeader h = hdr[c0 * 2 + 1];
+  if (h.state != 1) return;
+  const int rows = min(kRows, h.rows - h.rb * kRows);
+  if ((int)blockIdx.y * 16 >= rows) return;
+  const int end = last_part(hdr, c0);
+  const uint32_t r = a.hq / a.hkv;
+  for (int i = threadIdx.x; i < 16 * D / 4; i += 128) {
+    const int row = blockIdx.y * 16 + i / (D / 4), c = i % (D / 4) * 4;
+    if (row >= rows) break;
+    float m = -FLT_MAX, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = c0; p <= end; ++p) {
+      const RowsPart<D>& x = part[p * 2 + (p == c0)];
+      const float mx = x.m[row], now = fmaxf(m, mx), f0 = ex2(m - now), f1 = ex2(mx - now);
+      const float4 y = *reinterpret_cast<const float4*>(&x.o[row][c]);
+      o.x = fmaf(y.x, f1, o.x * f0);
+      o.y = fmaf(y.y, f1, o.y * f0);
+      o.z = fmaf(y.z, f1, o.z * f0);
+      o.w = fmaf(y.w, f1, o.w * f0);
+      l = fmaf(x.l[row], f1, l * f0);
+      m = now;
+    }
+    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const uint32_t at = h.rb * kRows + row, tok = at / r;
+    T* dst = static_cast<T*>(a.out) + ((int64_t)(h.q0 + tok) * a.hq + h.head * r + at - tok * r) * D + c;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack_out<T>(o.x * inv, o.y * inv), pack_out<T>(o.z * inv, o.w * inv));
+  }
+}
+
+template <typename T, int D, int G>
+cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
+  constexpr size_t bytes = Shape<D, G>::kSmem;
+  static_assert(bytes + sizeof(Control) + 64 <= 227 * 1024, "shared memory of a block");
+  static_assert(sizeof(RowsPart<D>) % 16 == 0, "parts are read in 16 bytes");
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  static std::atomic<uint64_t> allowed{0};  // devices on which the kernel may have this much shared memory
+  if (dev >= 64 || !(allowed.load(std::memory_order_relaxed) >> dev & 1)) {
+    e = cudaFuncSetAttribute(rows_kernel<T, D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) allowed.fetch_or(1ull << dev, std::memory_order_relaxed);
+  }
+  int shift = 4;
+  while ((1 << shift) < a.page) ++shift;
+  rows_kernel<T, D, G><<<kCtas, 32 * kWarps, bytes, st>>>(a, shift);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas, kRows / 16);
+  cfg.blockDim = dim3(128);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, rows_join_kernel<T, D>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_shape(const AttnArgs& a, cudaStream_t st) {
+  if (a.d == 64) return a.group == 32 ? launch<T, 64, 32>(a, st) : launch<T, 64, 64>(a, st);
+  if (a.group == 32) return launch<T, 128, 32>(a, st);
+  return a.group == 64 ? launch<T, 128, 64>(a, st) : launch<T, 128, 128>(a, st);
+}
+
+}  // namespace
+
+size_t attn_rows_workspace_bytes(int d) {
+  return 2 * kCtas * (sizeof(PartHeader) + (d == 64 ? sizeof(RowsPart<64>) : sizeof(RowsPart<128>)));
+}
+
+cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st) {
+  return a.type == FQ_F16 ? launch_shape<__half>(a, st) : launch_shape<__nv_bfloat16>(a, st);
+}
+
+cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count) {
+  return read_wait_counter(g_kv4_rows_wait_timeouts, clear, count);
+}
+
+}  // namespace kv4
+}  // namespace fq

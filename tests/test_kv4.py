@@ -120,8 +120,9 @@ def test_page_step_refuses(edit, status):
 
 def test_sizes():
     assert fq.fq_kv4_unit_bytes(96, 32) == 0 and fq.fq_kv4_unit_bytes(64, 128) == 0 and fq.fq_kv4_unit_bytes(128, 0) == 0
-    assert fq.fq_kv4_attn_workspace_bytes(64) > 0 and fq.fq_kv4_attn_workspace_bytes(128) > 0
-    assert fq.fq_kv4_attn_workspace_bytes(80) == 0
+    ws = fq.fq_kv4_attn_workspace_bytes
+    assert ws(8, 1, 64, 1) > 0 and ws(32, 8, 128, 1) > 0 and ws(32, 8, 128, 64) > ws(32, 8, 128, 1)
+    assert ws(8, 1, 80, 1) == 0 and ws(7, 2, 64, 1) == 0 and ws(8, 0, 64, 1) == 0 and ws(8, 1, 64, -1) == 0
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():
