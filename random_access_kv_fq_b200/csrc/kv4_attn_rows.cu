@@ -1,22 +1,23 @@
 // Attention over the 4-bit paged cache for many rows of a kv head (chunks of a prompt, drafted
 // tokens): 128 rows (query token, query head) at a time on the fifth-generation tensor cores.
 //
-// One block per SM, its warps in roles that meet in mbarriers:
-//   loader   copies units (bulk copies) into a ring of 64-token tiles of packed cache;
-//   unpack   4 warps turn a tile into fp16 operands in shared memory, two tiles deep;
+// One block per SM, its warps in roles that meet in mbarriers, over tiles of 128 tokens:
+//   loader   copies units (bulk copies) into a ring of packed cache;
+//   unpack   4 warps turn keys and 2 turn values into fp16 operands in shared memory, two tiles deep;
 //   mma      one thread issues tcgen05.mma: S = Q K^T into one of two buffers of tensor memory,
 //            O += P V with P in tensor memory, the next tile's S under this tile's softmax;
-//   softmax  4 warps, a thread to a row: S out of tensor memory, weights P back into it.
-// With codes c, steps s and zeros z, scores carry no 16-bit rounding of the keys: s is split into its
-// leading 7 bits and the rest, so that s_hi c and s_lo c are fp16 numbers exactly, and
+//   softmax  8 warps, two threads to a row: S out of tensor memory, weights P back into its place.
+// q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), half a step (2^-12) off.
+// For bf16 outputs, whose own rounding is 2^-9, keys and weights are fp16 numbers likewise.  For fp16
+// outputs neither may add to it:  s is split into its leading 7 bits and the rest, so that s_hi c and
+// s_lo c are fp16 numbers exactly, and
 //   S = Q (s_hi C)^T + Q (s_lo C)^T + qsum Z^T,
-// the last one a 16-wide product of the groups' sums of q (in two parts) with the zeros.  Values are
-// fp16(c s + z); weights are fp16, for fp16 outputs in two parts.  q is scaled to fp16 by a power of
-// two per row.  The softmax runs to base 2 against a maximum that moves only when a score passes it
-// by 8; moving it rescales O in tensor memory.
+// the last one a 16-wide product of the groups' sums of q (in two parts) with the zeros; weights are in
+// two parts, O = P_hi V + P_lo V.  The softmax runs to base 2 against a maximum that moves only when a
+// score passes it by 8; moving it rescales O in tensor memory.
 //
-// Per 64 tokens and 128 rows of d = 128 the tensor pipe needs about 800 cycles (1,056 with weights in
-// two parts), the softmax about 500 instructions of each of its warps.
+// A product of 128 x 128 x 16 takes 64 cycles (of 128 x 64 x 16: 50 to 57, so tiles are 128 tokens), so
+// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.
 #include <atomic>
 #include <cfloat>
 
@@ -30,12 +31,12 @@ namespace {
 __device__ unsigned int g_kv4_rows_wait_timeouts = 0;  // blocks whose bounded waits gave up
 
 constexpr int kRows = 128;      // rows of a block's item
-constexpr int kTile = 64;       // tokens of a tile
+constexpr int kTile = 128;      // tokens of a tile
 constexpr int kTileUnits = kTile / kUnit;
 constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
-constexpr int kRing = 3;        // packed tiles in flight
-constexpr int kUnpackWarps = 4;
-constexpr int kWarps = 4 + kUnpackWarps + 2;  // softmax (which own tensor memory lanes), unpack, mma, loader
+constexpr int kSoftmaxWarps = 8;  // warps w and w + 4 share 32 rows: columns below 64 and from 64 on
+constexpr int kKeyWarps = 4, kValueWarps = 2, kUnpackWarps = kKeyWarps + kValueWarps;
+constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 2;  // 16: 128 registers a thread
 
 template <int D>
 struct RowsPart {
@@ -43,22 +44,24 @@ struct RowsPart {
   float m[kRows], l[kRows];
 };
 
-template <int D, int G>
+template <int D, int G, bool EXACT>
 struct Shape {
   static constexpr int NG = D / G, UB = unit_bytes(D, G), KB = D / 32, NA = D / 64;
-  static constexpr int kK = kTile * D * 2;           // bytes of one fp16 operand of a tile
-  static constexpr int kZ = kTile * 32;              // zeros: 16 numbers a token
-  static constexpr int kBuf = 3 * kK + kZ;           // s_hi C, s_lo C, V, Z
-  static constexpr int kPacked = kTileUnits * UB;
-  static constexpr size_t kSmem = 1024 + 2 * kBuf + kRing * kPacked;
-  // tensor memory columns
-  static constexpr uint32_t S = 0, O = 128, Q = O + D, QZ = Q + D / 2, P = 352;  // P: [2][hi, lo][32]
-  static_assert(QZ + 8 <= P && P + 128 <= 512, "tensor memory");
+  static constexpr int kOp = kTile * D * 2;          // bytes of one fp16 operand of a tile
+  static constexpr int kZ = EXACT ? kTile * 32 : 0;  // zeros: 16 numbers a token
+  static constexpr int kK = (EXACT ? 2 : 1) * kOp + kZ, kBuf = kK + kOp;
+  static constexpr int kChunkUnits = D == 128 ? 2 : 4;  // units of a ring's stage: one step of 4 warps
+  static constexpr int kChunks = kTileUnits / kChunkUnits, kPacked = kChunkUnits * UB;
+  static constexpr int kRing = EXACT && D == 128 ? 4 : 8;  // what shared memory leaves
+  static constexpr size_t kControl = 1024;
+  static constexpr size_t kSmem = kControl + 2 * kBuf + kRing * kPacked;
+  // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
+  static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
 
 struct Control {
-  uint64_t ring_full[kRing], ring_empty[kRing];
-  uint64_t kv_full[2], pv_done[2], s_full[2], p_full[2], q_full;
+  uint64_t ring_full[8], ring_empty[8];
+  uint64_t k_full[2], v_full[2], pv_done[2], s_full[2], p_full[2], q_full, pair[4];
   uint32_t tmem;
   int gave_up;
   int gone[8];  // units of the last eight tiles that are not there (bits)
@@ -66,6 +69,7 @@ struct Control {
   int start_b;
   int64_t start_in;
 };
+static_assert(sizeof(Control) <= 1024, "in front of the operands");
 
 // A bounded wait that all of the block gives up together.
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
@@ -135,65 +139,67 @@ __device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) {
   c[3] = __hfma2(h2(and_or(w8, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
 }
 
-// This warp's share of a tile: steps of 32 lanes, each a 16-byte chunk (4 words) of a token's keys
-// or values.  K rows go K-major, V rows MN-major, both with the 128-byte swizzle; lanes are spread
-// so that no eight of them meet in a bank.
-template <int D, int G>
-__device__ __forceinline__ void unpack_tile(uint32_t packed, uint32_t buf, int warp, int lane, int pos0, int first, int end, int gone) {
-  using C = Shape<D, G>;
-  constexpr int kChunks = D / 32, kTokens = 32 / kChunks, kSteps = kTile / kTokens;
-#pragma unroll 1
-  for (int i = warp; i < kSteps; i += kUnpackWarps) {
-    const int ch = lane % kChunks, row = i * kTokens + lane / kChunks;  // row: place in the tile's packed order
-    const int unit = row / kUnit, place = row % kUnit;
-    const uint32_t u = packed + unit * C::UB;
-    uint32_t w[4], sc[C::NG];
-    // keys: packed row `place` holds token 0 4 1 5 2 6 3 7 (+ 8)
-    lds<16>(u + place * (D / 2) + ch * 16, w);
-    lds<4 * C::NG>(u + off_ks(D) + place * 4 * C::NG, sc);
-    const int tok = (place >> 1 & 3) + 4 * (place & 1) + (place & 8), n = unit * kUnit + tok;
-    const uint32_t krow = buf + n * 128;
+// Eight tokens' keys (16 for d = 64), from row `row` of a tile on: 32 lanes, each a 16-byte chunk (4
+// words) of a token.  Rows go K-major with the 128-byte swizzle; lanes are spread so that no eight of
+// them meet in a bank.
+template <int D, int G, bool EXACT>
+__device__ __forceinline__ void unpack_keys(uint32_t unit, uint32_t buf, int place, int ch, int row_unit) {
+  using C = Shape<D, G, EXACT>;
+  uint32_t w[4], sc[C::NG];
+  // packed row `place` holds token 0 4 1 5 2 6 3 7 (+ 8)
+  lds<16>(unit + place * (D / 2) + ch * 16, w);
+  lds<4 * C::NG>(unit + off_ks(D) + place * 4 * C::NG, sc);
+  const int n = row_unit + (place >> 1 & 3) + 4 * (place & 1) + (place & 8);
+  const uint32_t krow = buf + n * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int kb = j % C::KB, t = D == 128 ? ch : 2 * ch + (j >> 1), word = 4 * kb + t;
-      const int g = 32 * kb / G;
-      const uint32_t s = C::NG == 1 ? sc[0] & 0xFFFFu : (sc[g / 2] >> (16 * (g & 1))) & 0xFFFFu;
-      const uint32_t shi = s & 0xFFF0u;
-      const __half2 s_hi = h2(shi | shi << 16), s_all = h2(s | s << 16), s_lo = __hsub2(s_all, s_hi);
-      __half2 c[4];
-      codes(w[j], c);
-      const uint32_t at = krow + (word >> 3) * (kTile * 128) + (((word & 7) ^ (n & 7)) << 4);
-      sts16(at, u32(__hmul2(c[0], s_hi)), u32(__hmul2(c[1], s_hi)), u32(__hmul2(c[2], s_hi)), u32(__hmul2(c[3], s_hi)));
-      sts16(at + C::kK, u32(__hmul2(c[0], s_lo)), u32(__hmul2(c[1], s_lo)), u32(__hmul2(c[2], s_lo)), u32(__hmul2(c[3], s_lo)));
+  for (int j = 0; j < 4; ++j) {
+    const int kb = j % C::KB, t = D == 128 ? ch : 2 * ch + (j >> 1), word = 4 * kb + t;
+    const int g = 32 * kb / G;
+    const uint32_t s = C::NG == 1 ? __byte_perm(sc[0], 0, 0x1010) : __byte_perm(sc[g / 2], 0, g & 1 ? 0x3232 : 0x1010);
+    const uint32_t z = C::NG == 1 ? __byte_perm(sc[0], 0, 0x3232) : __byte_perm(sc[(C::NG + g) / 2], 0, g & 1 ? 0x3232 : 0x1010);
+    __half2 c[4];
+    codes(w[j], c);
+    const uint32_t at = krow + (word >> 3) * (kTile * 128) + (((word & 7) ^ (n & 7)) << 4);
+    if constexpr (EXACT) {
+      const __half2 hi = h2(s & 0xFFF0FFF0u), lo = __hsub2(h2(s), hi);
+      sts16(at, u32(__hmul2(c[0], hi)), u32(__hmul2(c[1], hi)), u32(__hmul2(c[2], hi)), u32(__hmul2(c[3], hi)));
+      sts16(at + C::kOp, u32(__hmul2(c[0], lo)), u32(__hmul2(c[1], lo)), u32(__hmul2(c[2], lo)), u32(__hmul2(c[3], lo)));
+    } else {
+      sts16(at, u32(__hfma2(c[0], h2(s), h2(z))), u32(__hfma2(c[1], h2(s), h2(z))), u32(__hfma2(c[2], h2(s), h2(z))),
+            u32(__hfma2(c[3], h2(s), h2(z))));
     }
-    if (ch == 0) {
-      // zeros twice (for the two parts of the sums of q), then nothing
-      const uint32_t at = buf + 3 * C::kK + ptx::noswz16_offset(n, 0);
-      if constexpr (C::NG == 4) sts16(at, sc[2], sc[3], sc[2], sc[3]);
-      else if constexpr (C::NG == 2) sts16(at, sc[1], sc[1], 0, 0);
-      else sts16(at, __byte_perm(sc[0], 0, 0x3232), 0, 0, 0);
-    }
-    // values: packed row = token
-    uint32_t sz = 0;
-    lds<16>(u + off_v(D) + place * (D / 2) + ch * 16, w);
-    const int group = D == 128 ? ch ^ (place & 2) : ch;  // 32 coordinates
-    lds<4>(u + off_vs(D, G) + (place * C::NG + group * 32 / G) * 4, &sz);
-    const int pos = pos0 + row;
-    if (pos < first || pos >= end || (gone >> unit & 1)) sz = 0;  // nobody sees it: its value becomes 0
-    if (D == 128 && (group & 2)) {
-      uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
-      x = w[1]; w[1] = w[3]; w[3] = x;
-    }
-    const __half2 st = h2(__byte_perm(sz, 0, 0x1010)), ze = h2(__byte_perm(sz, 0, 0x3232));
-    const uint32_t vrow = buf + 2 * C::kK + (row >> 3) * (C::NA * 1024) + (row & 7) * 128;
+  }
+  if (EXACT && ch == 0) {
+    // zeros twice (for the two parts of the sums of q), then nothing
+    const uint32_t at = buf + 2 * C::kOp + ptx::noswz16_offset(n, 0);
+    if constexpr (C::NG == 4) sts16(at, sc[2], sc[3], sc[2], sc[3]);
+    else if constexpr (C::NG == 2) sts16(at, sc[1], sc[1], 0, 0);
+    else sts16(at, __byte_perm(sc[0], 0, 0x3232), 0, 0, 0);
+  }
+}
+
+// The same of values: rows go MN-major.  seen: somebody sees the token; its values are 0 otherwise.
+template <int D, int G, bool EXACT>
+__device__ __forceinline__ void unpack_values(uint32_t unit, uint32_t buf, int place, int ch, int row, bool seen) {
+  using C = Shape<D, G, EXACT>;
+  uint32_t w[4], sz;
+  lds<16>(unit + off_v(D) + place * (D / 2) + ch * 16, w);
+  const int group = D == 128 ? ch ^ (place & 2) : ch;  // 32 coordinates
+  lds<4>(unit + off_vs(D, G) + (place * C::NG + group * 32 / G) * 4, &sz);
+  if (!seen) sz = 0;
+  if (D == 128 && (group & 2)) {
+    uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
+    x = w[1]; w[1] = w[3]; w[3] = x;
+  }
+  const __half2 st = h2(__byte_perm(sz, 0, 0x1010)), ze = h2(__byte_perm(sz, 0, 0x3232));
+  const uint32_t vrow = buf + (row >> 3) * (C::NA * 1024) + (row & 7) * 128;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int word = 4 * group + (D == 128 ? j ^ (group & 2) : j);
-      __half2 c[4];
-      codes(w[j], c);
-      sts16(vrow + (word >> 3) * 1024 + (((word & 7) ^ (row & 7)) << 4), u32(__hfma2(c[0], st, ze)), u32(__hfma2(c[1], st, ze)),
-            u32(__hfma2(c[2], st, ze)), u32(__hfma2(c[3], st, ze)));
-    }
+  for (int j = 0; j < 4; ++j) {
+    const int word = 4 * group + (D == 128 ? j ^ (group & 2) : j);
+    __half2 c[4];
+    codes(w[j], c);
+    sts16(vrow + (word >> 3) * 1024 + (((word & 7) ^ (row & 7)) << 4), u32(__hfma2(c[0], st, ze)), u32(__hfma2(c[1], st, ze)),
+          u32(__hfma2(c[2], st, ze)), u32(__hfma2(c[3], st, ze)));
   }
 }
 
@@ -201,11 +207,13 @@ __device__ __forceinline__ void unpack_tile(uint32_t packed, uint32_t buf, int w
 
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int page_shift) {
-  using C = Shape<D, G>;
-  constexpr bool kTwoParts = __is_same(T, __half);
-  extern __shared__ uint8_t raw_smem[];
-  __shared__ Control ctl;
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+  constexpr bool kExact = __is_same(T, __half);
+  using C = Shape<D, G, kExact>;
+  constexpr int kRing = C::kRing;
+  extern __shared__ __align__(1024) uint8_t raw_smem[];
+  __shared__ float row_max[2][2][kRows];  // [tile's parity][half of the columns]
+  Control& ctl = *reinterpret_cast<Control*>(raw_smem);
+  uint8_t* smem = raw_smem + C::kControl;
   uint8_t* packed = smem + 2 * C::kBuf;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = a.hq / a.hkv;
@@ -213,16 +221,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   if (tid == 0) {
     ctl.gave_up = 0;
     for (int i = 0; i < kRing; ++i) {
-      ptx::mbar_init(&ctl.ring_full[i], kTileUnits);
+      ptx::mbar_init(&ctl.ring_full[i], C::kChunkUnits);
       ptx::mbar_init(&ctl.ring_empty[i], kUnpackWarps);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl.kv_full[i], kUnpackWarps);
+      ptx::mbar_init(&ctl.k_full[i], kKeyWarps);
+      ptx::mbar_init(&ctl.v_full[i], kValueWarps);
       ptx::mbar_init(&ctl.pv_done[i], 1);
       ptx::mbar_init(&ctl.s_full[i], 1);
-      ptx::mbar_init(&ctl.p_full[i], 4);
+      ptx::mbar_init(&ctl.p_full[i], kSoftmaxWarps);
     }
     ptx::mbar_init(&ctl.q_full, 4);
+    for (int i = 0; i < 4; ++i) ptx::mbar_init(&ctl.pair[i], 2);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -230,8 +240,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     ptx::tmem_relinquish();
   }
   // the upper half of the zeros' 16 numbers is never written again
-  for (int i = tid; i < 2 * kTile; i += 32 * kWarps)
-    sts16(ptx::smem_u32(smem) + (i / kTile) * C::kBuf + 3 * C::kK + ptx::noswz16_offset(i % kTile, 8), 0, 0, 0, 0);
+  if (kExact)
+    for (int i = tid; i < 2 * kTile; i += 32 * kWarps)
+      sts16(ptx::smem_u32(smem) + (i / kTile) * C::kBuf + 2 * C::kOp + ptx::noswz16_offset(i % kTile, 8), 0, 0, 0, 0);
   ptx::fence_proxy_async_smem();
 
   // The line of all items' costs, cut into one range per block; the thread whose sequences hold the
@@ -293,14 +304,28 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   uint32_t tile = 0;  // tiles so far, over all items: buffers and parities
   PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
 
-  if (warp < 4) {
+  if (warp < kSoftmaxWarps) {
     // ---------------------------------------------------------------- softmax
     RowsPart<D>* out_part = reinterpret_cast<RowsPart<D>*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
-    const uint32_t lanes = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const int half = warp >> 2, my_row = tid & (kRows - 1);
     int left_part[2] = {0, 0};
+    uint32_t meets = 0;  // of the two warps that share rows
     bool ok = true;
+    // gives the other warp a number per row and takes its own; both see all that was done before
+    const auto swap = [&](float x, float& y) {
+      row_max[meets & 1][half][my_row] = x;
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&ctl.pair[warp & 3]);
+      const bool met = __all_sync(~0u, wait(&ctl, &ctl.pair[warp & 3], meets));
+      ptx::tc_fence_after();
+      if (met) y = row_max[meets & 1][half ^ 1][my_row];
+      ++meets;
+      return met;
+    };
     for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
-      const uint32_t row = it.rb * kRows + tid;
+      const uint32_t row = it.rb * kRows + my_row;
       const bool in = row < (uint32_t)it.s.rows;
       const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
       float m = -FLT_MAX, l = 0.f, kappa = 0.f;
@@ -338,84 +363,90 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           down = -down;
         }
         kappa = fmaxf(kappa, 1e-37f);  // so that -inf, a masked score, stays that
-        float sum[C::NG];
+        if (half == 0) {
+          float sum[C::NG];
 #pragma unroll
-        for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
+          for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
 #pragma unroll
-        for (int w4 = 0; w4 < D / 8; w4 += 4) {  // 32 coordinates: 16 columns
-          uint32_t col[16];
+          for (int w4 = 0; w4 < D / 8; w4 += 4) {  // 32 coordinates: 16 columns
+            uint32_t col[16];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint4 v = word(w4 + i);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            __half y[8];
+            for (int i = 0; i < 4; ++i) {
+              const uint4 v = word(w4 + i);
+              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+              __half y[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              y[k] = __float2half_rn(q_float<T>((uint16_t)(x[k / 2] >> (16 * (k & 1)))) * down);
-              sum[8 * w4 / G] += __half2float(y[k]);
+              for (int k = 0; k < 8; ++k) {
+                y[k] = __float2half_rn(q_float<T>((uint16_t)(x[k / 2] >> (16 * (k & 1)))) * down);
+                sum[8 * w4 / G] += __half2float(y[k]);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) col[4 * i + k] = u32(__halves2half2(y[k], y[k + 4]));
             }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) col[4 * i + k] = u32(__halves2half2(y[k], y[k + 4]));
+            __syncwarp();
+            ptx::tmem_st16(lanes + C::Q + 4 * w4, col);
           }
+          if (kExact) {
+            uint32_t qz[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            __half part[2][C::NG];
+#pragma unroll
+            for (int i = 0; i < C::NG; ++i) {
+              part[0][i] = __float2half_rn(sum[i]);
+              part[1][i] = __float2half_rn(sum[i] - __half2float(part[0][i]));
+            }
+            if constexpr (C::NG == 1) {
+              qz[0] = u32(__halves2half2(part[0][0], part[1][0]));
+            } else {
+#pragma unroll
+              for (int p = 0; p < 2; ++p)
+#pragma unroll
+                for (int i = 0; i < C::NG; i += 2) qz[(p * C::NG + i) / 2] = u32(__halves2half2(part[p][i], part[p][i + 1]));
+            }
+            ptx::tmem_st8(lanes + C::QZ, qz);
+          }
+          ptx::tmem_wait_st();
+          ptx::tc_fence_before();
           __syncwarp();
-          ptx::tmem_st16(lanes + C::Q + 4 * w4, col);
+          if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
         }
-        uint32_t qz[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        __half part[2][C::NG];
-#pragma unroll
-        for (int i = 0; i < C::NG; ++i) {
-          part[0][i] = __float2half_rn(sum[i]);
-          part[1][i] = __float2half_rn(sum[i] - __half2float(part[0][i]));
-        }
-        if constexpr (C::NG == 1) {
-          qz[0] = u32(__halves2half2(part[0][0], part[1][0]));
-        } else {
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int i = 0; i < C::NG; i += 2) qz[(p * C::NG + i) / 2] = u32(__halves2half2(part[p][i], part[p][i + 1]));
-        }
-        ptx::tmem_st8(lanes + C::QZ, qz);
-        ptx::tmem_wait_st();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
 
         for (int j = it.t0; j < it.t1; ++j, ++tile) {
-          const uint32_t buf = tile & 1;
-          ok = wait(&ctl, &ctl.s_full[buf], tile >> 1);
-          ok = __all_sync(~0u, ok);
+          const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf;
+          ok = __all_sync(~0u, wait(&ctl, &ctl.s_full[buf], tile >> 1));
           if (!ok) break;
           ptx::tc_fence_after();
           uint32_t sr[64];
-          ptx::tmem_ld_cols<0, 64>(lanes + C::S + 64 * buf, sr);
+          ptx::tmem_ld_cols<0, 64>(sp + 64 * half, sr);
           ptx::tmem_wait_ld();
-          const int pos0 = it.base_u * kUnit + j * kTile;
-          // what this row sees of the tile: columns [c0, c1), less units that are not there
-          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[tile & 7];
-          if (__any_sync(~0u, c0 > 0 || c1 < kTile || gone != 0)) {
+          const int pos0 = it.base_u * kUnit + j * kTile + 64 * half;
+          // what this row sees of these columns: [c0, c1), less units that are not there
+          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[tile & 7] >> (4 * half) & 15;
+          if (__any_sync(~0u, c0 > 0 || c1 < 64 || gone != 0)) {
 #pragma unroll
-            for (int c = 0; c < kTile; ++c)
+            for (int c = 0; c < 64; ++c)
               if (c < c0 || c >= c1 || (gone >> (c / kUnit) & 1)) sr[c] = 0xFF800000u;
           }
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < kTile; c += 8)
+          for (int c = 0; c < 64; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(sr[c + i])), __uint_as_float(sr[c + 4 + i]));
-          const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * kappa;
+          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * kappa, other = 0.f;
+          ok = swap(top, other);  // both halves of S are in registers now: P may take its place
+          if (!ok) break;
+          top = fmaxf(top, other);
           if (__any_sync(~0u, top > m + 8.f)) {
             const float now = fmaxf(m, top), f = ex2(m - now);
             m = now;
             l *= f;
             if (j > it.t0) {
-              // O is this warp's once the tile before is in it
+              // O is the softmax's once the tile before is in it; each warp takes half of the columns
               ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1));
               if (!ok) break;
               ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                 uint32_t o[16];
                 ptx::tmem_ld16(lanes + C::O + c, o);
                 ptx::tmem_wait_ld();
@@ -427,14 +458,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
             }
           }
           float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-          // P of this buffer was used two tiles ago
-          if (tile >= 2) {
-            ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[buf], (tile - 2) >> 1));
-            if (!ok) break;
-            ptx::tc_fence_after();
-          }
 #pragma unroll
-          for (int c = 0; c < kTile; c += 32) {
+          for (int c = 0; c < 64; c += 32) {
             uint32_t p[16], pl[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -443,13 +468,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
               sum4[i & 3] += x + y;
               const __half2 v = __floats2half2_rn(x, y);
               p[i] = u32(v);
-              if (kTwoParts) {
+              if (kExact) {
                 const float2 back = __half22float2(v);
                 pl[i] = u32(__floats2half2_rn(x - back.x, y - back.y));
               }
             }
-            ptx::tmem_st16(lanes + C::P + 64 * buf + c / 2, p);
-            if (kTwoParts) ptx::tmem_st16(lanes + C::P + 64 * buf + 32 + c / 2, pl);
+            ptx::tmem_st16(sp + 32 * half + c / 2, p);
+            if (kExact) ptx::tmem_st16(sp + 64 + 32 * half + c / 2, pl);
           }
           l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
           ptx::tmem_wait_st();
@@ -458,8 +483,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           if (lane == 0) ptx::mbar_arrive(&ctl.p_full[buf]);
         }
         if (!ok) break;
-        ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1));
+        float other = 0.f;
+        ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1)) && swap(l, other);
         if (!ok) break;
+        l += other;
         ptx::tc_fence_after();
       }
       const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.s.cost;
@@ -468,7 +495,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
       T* dst = static_cast<T*>(a.out) + ((int64_t)(it.s.q0 + tok) * a.hq + it.head * r + hh) * D;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 16) {
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         uint32_t o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0;
@@ -488,63 +515,86 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                                                                 pack_out<T>(v[i + 4] * inv, v[i + 5] * inv), pack_out<T>(v[i + 6] * inv, v[i + 7] * inv));
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&part->o[tid][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&part->o[my_row][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
       if (!whole) {
-        if (in) {
-          part->m[tid] = m;
-          part->l[tid] = l;
+        if (in && half == 0) {
+          part->m[my_row] = m;
+          part->l[my_row] = l;
         }
         left_part[k] = 1;
         if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{it.to == it.s.cost ? 3 : 1, it.s.q0, it.s.rows, it.head, it.rb};
       }
-      ptx::tc_fence_before();  // O is read before the next item's products
+      // O is read before the next item's first product: its q comes after both warps met here
+      if (any) {
+        float none;
+        ok = swap(0.f, none);
+      }
     }
     if (tid == 0)
       for (int k = 0; k < 2; ++k)
         if (!left_part[k]) out_hdr[blockIdx.x * 2 + k].state = 0;
-  } else if (warp < 4 + kUnpackWarps) {
+  } else if (warp < kSoftmaxWarps + kUnpackWarps) {
     // ---------------------------------------------------------------- unpack
+    constexpr int kStep = 1024 / D;  // tokens of a warp's step
+    const bool keys = warp < kSoftmaxWarps + kKeyWarps;
+    const int ch = lane % (D / 32), row_lane = lane / (D / 32);
+    uint32_t chunk = 0;
     bool ok = true;
     for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
-      for (int j = it.t0; j < it.t1; ++j, ++tile) {
-        const uint32_t slot = tile % kRing, buf = tile & 1;
-        ok = wait(&ctl, &ctl.ring_full[slot], tile / kRing);
-        if (ok && tile >= 2) ok = wait(&ctl, &ctl.pv_done[buf], (tile - 2) >> 1);
-        ok = __all_sync(~0u, ok);
+      for (int j = it.t0; j < it.t1 && ok; ++j, ++tile) {
+        const uint32_t buf = tile & 1, base = smem32 + buf * C::kBuf;
+        // keys are done with when their scores are, values when the products with the weights are
+        if (tile >= 2) ok = __all_sync(~0u, wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1));
+        for (int c = 0; c < C::kChunks && ok; ++c, ++chunk) {
+          const uint32_t slot = chunk % kRing;
+          ok = __all_sync(~0u, wait(&ctl, &ctl.ring_full[slot], chunk / kRing));
+          if (!ok) break;
+          const uint32_t units = packed32 + slot * C::kPacked;
+          const int row0 = c * C::kChunkUnits * kUnit;  // of the tile
+          if (keys) {
+            const int row = (warp - kSoftmaxWarps) * kStep + row_lane;
+            unpack_keys<D, G, kExact>(units + row / kUnit * C::UB, base, row % kUnit, ch, row0 + (row & ~(kUnit - 1)));
+          } else {
+            const int gone = *(volatile int*)&ctl.gone[tile & 7];
+#pragma unroll
+            for (int i = 0; i < kKeyWarps / kValueWarps; ++i) {
+              const int row = ((warp - kSoftmaxWarps - kKeyWarps) * (kKeyWarps / kValueWarps) + i) * kStep + row_lane;
+              const int pos = it.base_u * kUnit + j * kTile + row0 + row;
+              unpack_values<D, G, kExact>(units + row / kUnit * C::UB, base + C::kK, row % kUnit, ch, row0 + row,
+                                          pos >= it.first && pos < it.end && !(gone >> ((row0 + row) / kUnit) & 1));
+            }
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&ctl.ring_empty[slot]);
+        }
         if (!ok) break;
-        const uint32_t at = packed32 + slot * C::kPacked;
-        unpack_tile<D, G>(at, smem32 + buf * C::kBuf, warp - 4, lane, it.base_u * kUnit + j * kTile, it.first, it.end,
-                          *(volatile int*)&ctl.gone[tile & 7]);
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          ptx::mbar_arrive(&ctl.kv_full[buf]);
-          ptx::mbar_arrive(&ctl.ring_empty[slot]);
-        }
+        if (lane == 0) ptx::mbar_arrive(keys ? &ctl.k_full[buf] : &ctl.v_full[buf]);
       }
     }
-  } else if (warp == 4 + kUnpackWarps) {
+  } else if (warp == kSoftmaxWarps + kUnpackWarps) {
     // ---------------------------------------------------------------- mma
     constexpr uint32_t idesc_s = ptx::idesc_f16_f32(128, kTile), idesc_o = ptx::idesc_f16_f32(128, D) | (1u << 16);
     bool ok = true;
     uint32_t item = 0;
     auto scores = [&](uint32_t t) {  // S of tile t
-      const uint32_t buf = t & 1, base = smem32 + buf * C::kBuf, d = tmem + C::S + 64 * buf;
+      const uint32_t buf = t & 1, base = smem32 + buf * C::kBuf, d = tmem + C::S + 128 * buf;
 #pragma unroll
-      for (int part = 0; part < 2; ++part)
+      for (int part = 0; part < (kExact ? 2 : 1); ++part)
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)
-          ptx::umma_f16_ts(d, tmem + C::Q + 8 * ks, ptx::sdesc_kmajor_sw128(base + part * C::kK + (ks >> 2) * (kTile * 128) + (ks & 3) * 32),
+          ptx::umma_f16_ts(d, tmem + C::Q + 8 * ks, ptx::sdesc_kmajor_sw128(base + part * C::kOp + (ks >> 2) * (kTile * 128) + (ks & 3) * 32),
                            idesc_s, part > 0 || ks > 0 ? 1u : 0u);
-      ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 3 * C::kK, 128, 256), idesc_s, 1u);
+      if (kExact) ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 2 * C::kOp, 128, 256), idesc_s, 1u);
       ptx::umma_commit(&ctl.s_full[buf]);
     };
     for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
       if (it.t0 >= it.t1) continue;
       if (lane == 0) {
-        ok = wait(&ctl, &ctl.q_full, item) && wait(&ctl, &ctl.kv_full[tile & 1], tile >> 1);
+        ok = wait(&ctl, &ctl.q_full, item) && wait(&ctl, &ctl.k_full[tile & 1], tile >> 1);
         if (ok) {
           ptx::tc_fence_after();
           scores(tile);
@@ -552,20 +602,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         for (int j = it.t0; j < it.t1 && ok; ++j) {
           const uint32_t t = tile + (j - it.t0), buf = t & 1;
           if (j + 1 < it.t1) {
-            ok = wait(&ctl, &ctl.kv_full[buf ^ 1], (t + 1) >> 1);
+            // the next tile's scores take the place of the weights of the tile before
+            ok = wait(&ctl, &ctl.k_full[buf ^ 1], (t + 1) >> 1) && (t == 0 || wait(&ctl, &ctl.pv_done[buf ^ 1], (t - 1) >> 1));
             if (!ok) break;
             ptx::tc_fence_after();
             scores(t + 1);
           }
-          ok = wait(&ctl, &ctl.p_full[buf], t >> 1);
+          ok = wait(&ctl, &ctl.v_full[buf], t >> 1) && wait(&ctl, &ctl.p_full[buf], t >> 1);
           if (!ok) break;
           ptx::tc_fence_after();
-          const uint32_t v = smem32 + buf * C::kBuf + 2 * C::kK;
+          const uint32_t v = smem32 + buf * C::kBuf + C::kK;
 #pragma unroll
-          for (int part = 0; part < (kTwoParts ? 2 : 1); ++part)
+          for (int part = 0; part < (kExact ? 2 : 1); ++part)
 #pragma unroll
             for (int ks = 0; ks < kTile / 16; ++ks)
-              ptx::umma_f16_ts(tmem + C::O, tmem + C::P + 64 * buf + 32 * part + 8 * ks,
+              ptx::umma_f16_ts(tmem + C::O, tmem + C::S + 128 * buf + 64 * part + 8 * ks,
                                ptx::sdesc_mnmajor_sw128(v + ks * 2 * C::NA * 1024, 1024, C::NA * 1024), idesc_o,
                                j > it.t0 || part > 0 || ks > 0 ? 1u : 0u);
           ptx::umma_commit(&ctl.pv_done[buf]);
@@ -579,31 +630,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     // ---------------------------------------------------------------- loader
     bool ok = true;
     const int shift = page_shift - 4;
+    uint32_t chunk = 0;
     for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
       const int32_t* table = a.tables + (int64_t)it.b * a.max_blocks;
       const int u_begin = it.base_u + it.t0 * kTileUnits, u_end = min(it.base_u + it.t1 * kTileUnits, (it.end + kUnit - 1) / kUnit);
       auto entry = [&](int u) { return u < u_end ? __ldg(table + (u >> shift)) : -1; };
       // lane i holds the table entry of units i, i + 32, ... of the part; the next 32 are on their way
       int id = -1, id_next = it.t0 < it.t1 ? entry(u_begin + lane) : -1;
-      for (int j = it.t0; j < it.t1; ++j, ++tile) {
-        const int at = ((j - it.t0) * kTileUnits) & 31;
+      for (int j = 0; j < (it.t1 - it.t0) * C::kChunks; ++j, ++chunk) {
+        const int at = (j * C::kChunkUnits) & 31;
         if (at == 0) {
           id = id_next;
-          id_next = entry(u_begin + (j - it.t0) * kTileUnits + 32 + lane);
+          id_next = entry(u_begin + j * C::kChunkUnits + 32 + lane);
         }
-        const uint32_t slot = tile % kRing;
-        if (tile >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[slot], tile / kRing - 1));
+        const uint32_t slot = chunk % kRing;
+        if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[slot], chunk / kRing - 1));
         if (!ok) break;
         const bool good = id >= 0 && id < a.n_blocks;
-        const uint32_t there = __ballot_sync(~0u, good) >> at;
-        // This place is free: the tile three back is unpacked, so the products of the one five back are
-        // done, and the softmax is past the one eight back.
-        if (lane == at) *(volatile int*)&ctl.gone[tile & 7] = ~there & ((1 << kTileUnits) - 1);
+        const uint32_t there = __ballot_sync(~0u, good) >> (at & ~(kTileUnits - 1));
+        // A tile's first chunk brings its mask.  The place is free: values of a tile at most four back are
+        // being unpacked, so the products of one six back are done and the softmax is past the one eight back.
+        if (j % C::kChunks == 0 && lane == at) *(volatile int*)&ctl.gone[(chunk / C::kChunks) & 7] = ~there & ((1 << kTileUnits) - 1);
         __syncwarp();
         const int i = lane - at;
-        if ((unsigned)i < kTileUnits) {
+        if ((unsigned)i < C::kChunkUnits) {
           if (good) {
-            const int u = u_begin + (j - it.t0) * kTileUnits + i;
+            const int u = u_begin + j * C::kChunkUnits + i;
             const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
             ptx::mbar_arrive_expect_tx(&ctl.ring_full[slot], C::UB);
             ptx::bulk_load(packed + slot * C::kPacked + i * C::UB, src, C::UB, &ctl.ring_full[slot]);
@@ -616,7 +668,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     }
     // copies in flight land before the block ends, also where a wait gave up
     if (!ok)
-      for (uint32_t t = tile > kRing ? tile - kRing : 0; t < tile; ++t) ptx::mbar_wait(&ctl.ring_full[t % kRing], (t / kRing) & 1);
+      for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[t % kRing], (t / kRing) & 1);
   }
 
   ptx::tc_fence_before();
@@ -671,8 +723,8 @@ __global__ void __launch_bounds__(128) rows_join_kernel(AttnArgs a) {
 
 template <typename T, int D, int G>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
-  constexpr size_t bytes = Shape<D, G>::kSmem;
-  static_assert(bytes + sizeof(Control) + 64 <= 227 * 1024, "shared memory of a block");
+  constexpr size_t bytes = Shape<D, G, __is_same(T, __half)>::kSmem;
+  static_assert(bytes + 4 * 2 * 2 * kRows <= 227 * 1024, "shared memory of a block");
   static_assert(sizeof(RowsPart<D>) % 16 == 0, "parts are read in 16 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

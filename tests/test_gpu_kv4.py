@@ -6,6 +6,9 @@ A = sum_t p_t |v_t| per coordinate and S = max_t sum_i |q_i k_ti| scale, an outp
   2^-11 A          values and weights are each rounded to fp16 once (half a step, 2^-12, each),
   2 (d + 8) 2^-23 S A   a score is a sum of d products in 32 bits, each addition off by at most
                    2^-23 of the sum of magnitudes; an error x of the scores moves the weights by 2x,
+  2^-11 S A        bf16 outputs of more than 16 rows of a kv head: keys are fp16 numbers too, half a
+                   step (2^-12) off, which moves a score by at most 2^-12 S and the weights by twice
+                   that (fp16 outputs, and fewer rows, take the keys as they are),
   2^-10 A / 16     exponentials, sums of weights and of weighted values in 32 bits, added step by
                    step (2^-23 for each of at most 2^9 additions),
   2^-24 (15 s + |z| where it is tiny)   fp16 values below 2^-14 have a fixed step: 2^-25 each."""
@@ -32,9 +35,10 @@ def _cpu(t):
     return t.detach().cpu().numpy()
 
 
-def _check_attn(out, want, A, S, d, dtype):
+def _check_attn(out, want, A, S, d, dtype, rows=1):
     got = _cpu(out.double())
-    bound = HALF_EPS[dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + 2 * (d + 8) * 2.0 ** -23 * S[..., None]) * A + 2.0 ** -24
+    per_score = 2 * (d + 8) * 2.0 ** -23 + (2.0 ** -11 if dtype == torch.bfloat16 and rows > 16 else 0)
+    bound = HALF_EPS[dtype] * np.abs(want) + (2.0 ** -11 + 2.0 ** -14 + per_score * S[..., None]) * A + 2.0 ** -24
     bad = ~(np.abs(got - want) <= bound)
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], bound[bad][:5])
 
@@ -92,9 +96,10 @@ def _attend(c, q, qlens=None, window=0, scale=None, **kw):
     cu = None if qlens is None else np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
     dt = q.dtype
     want = ref.attend(_cpu(q.double()), c.host, c.tables, c.lens, c.group, cu, window, scale)
+    max_q = 1 if cu is None else int(max(qlens, default=0))
     out = fq.fq_kv4_attn(q, _dev(c.host), _dev(c.tables), _dev(c.lens), c.group, cu_q=None if cu is None else _dev(cu),
-                         max_q=1 if cu is None else int(max(qlens, default=0)), window=window, scale=scale, **kw)
-    _check_attn(out, *want, c.d, dt)
+                         max_q=max_q, window=window, scale=scale, **kw)
+    _check_attn(out, *want, c.d, dt, rows=max_q * q.shape[1] // c.hkv)
     return out
 
 
@@ -201,11 +206,47 @@ def test_ragged_queries_and_windows(d, group, window, dtype):
     assert not out[row:row + 2].any() and out[row + 2:row + 5].any()
 
 
-@pytest.mark.parametrize("hq,hkv,m", [(8, 8, 70), (4, 1, 65), (7, 1, 33), (32, 2, 20)])
-def test_prefill_of_many_query_tokens(hq, hkv, m):
+@pytest.mark.parametrize("hq,hkv,m", [(8, 8, 70), (4, 1, 65), (7, 1, 33), (32, 2, 20), (2, 1, 300)])
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_prefill_of_many_query_tokens(hq, hkv, m, d, group, dtype):
     rng = np.random.default_rng(m)
-    c = Cache(rng, [m, m + 75], hkv, 128, 64, 32)
-    _attend(c, _q(rng, 2 * m - 3, hq, 128, torch.float16), qlens=[m, m - 3])
+    c = Cache(rng, [m, m + 75], hkv, d, group, 32)
+    _attend(c, _q(rng, 2 * m - 3, hq, d, dtype), qlens=[m, m - 3])
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("window", [0, 900])
+def test_chunks_over_long_contexts_that_span_blocks(dtype, window):
+    """A few items of many tiles: every block of the grid holds a part of one."""
+    rng = np.random.default_rng(21)
+    c = Cache(rng, [9001, 4500], 2, 64, 32, 64)
+    _attend(c, _q(rng, 12, 20, 64, dtype), qlens=[5, 7], window=window)
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_chunks_with_missing_pages_rising_maxima_and_odd_scales(dtype):
+    rng = np.random.default_rng(22)
+    c = Cache(rng, [700, 333, 0, 130], 1, 128, 32, 16)
+    c.tables[0, [0, 7, 8, 20, 43]] = -1
+    c.tables[1, ::2] = c.n_blocks
+    c.tables[3] = 2 ** 31 - 1
+    q = _q(rng, 40, 8, 128, dtype)
+    qlens = [10, 20, 3, 7]
+    for scale in (None, 0.0, -0.05, 2.0, 1e-30):
+        _attend(c, q, qlens=qlens, scale=scale)
+    # keys that grow along the context: the maximum moves in every tile
+    c.k *= np.linspace(0.1, 9, len(c.k), dtype=np.float32)[:, None, None].astype(c.k.dtype)
+    lens, pages = c.lens.tolist(), [-(-int(n) // 16) for n in c.lens]
+    c.tables[:] = -1
+    ids = rng.permutation(c.n_blocks)
+    at = 0
+    for b, m in enumerate(pages):
+        c.tables[b, :m] = ids[at:at + m]
+        at += m
+    c.fill(np.concatenate([c.tables[b, np.arange(n) // 16].astype(np.int64) * 16 + np.arange(n) % 16 for b, n in enumerate(lens)]))
+    _attend(c, q, qlens=qlens, scale=0.3)
+    _attend(c, q, qlens=qlens, scale=0.3, window=50)
 
 
 def test_rows_of_no_sequence_are_left_alone_and_bad_counts_stay_in_bounds():
