@@ -2,11 +2,12 @@
 // tokens): 128 rows (query token, query head) at a time on the fifth-generation tensor cores.
 //
 // One block per SM, its warps in roles that meet in mbarriers, over tiles of 128 tokens:
-//   loader   copies units (bulk copies) into a ring of packed cache;
-//   unpack   4 warps turn keys and 2 turn values into fp16 operands in shared memory, two tiles deep;
+//   loaders  copy the units' keys and their values (bulk copies) into a ring each of packed cache;
+//   unpack   8 warps turn keys and 4 turn values into fp16 operands in shared memory, two tiles deep;
 //   mma      one thread issues tcgen05.mma: S = Q K^T into one of two buffers of tensor memory,
 //            O += P V with P in tensor memory, the next tile's S under this tile's softmax;
-//   softmax  8 warps, two threads to a row: S out of tensor memory, weights P back into its place.
+//   softmax  16 warps, four threads to a row: S out of tensor memory, weights P back into its place.
+// All of them run one long chain of short instructions each, so there are as many as 64 registers allow.
 // q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), half a step (2^-12) off.
 // For bf16 outputs, whose own rounding is 2^-9, keys and weights are fp16 numbers likewise.  For fp16
 // outputs neither may add to it:  s is split into its leading 7 bits and the rest, so that s_hi c and
@@ -34,9 +35,9 @@ constexpr int kRows = 128;      // rows of a block's item
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kTileUnits = kTile / kUnit;
 constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
-constexpr int kSoftmaxWarps = 8;  // warps w and w + 4 share 32 rows: columns below 64 and from 64 on
-constexpr int kKeyWarps = 4, kValueWarps = 2, kUnpackWarps = kKeyWarps + kValueWarps;
-constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 2;  // 16: 128 registers a thread
+constexpr int kSoftmaxWarps = 16;  // warps w, w + 4, .. share 32 rows, 32 columns each
+constexpr int kKeyWarps = 8, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueWarps;
+constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 3;
 
 template <int D>
 struct RowsPart {
@@ -51,35 +52,43 @@ struct Shape {
   static constexpr int kZ = EXACT ? kTile * 32 : 0;  // zeros: 16 numbers a token
   static constexpr int kK = (EXACT ? 2 : 1) * kOp + kZ, kBuf = kK + kOp;
   static constexpr int kChunkUnits = D == 128 ? 2 : 4;  // units of a ring's stage: one step of 4 warps
-  static constexpr int kChunks = kTileUnits / kChunkUnits, kPacked = kChunkUnits * UB;
+  static constexpr int kChunks = kTileUnits / kChunkUnits, kCodes = kChunkUnits * kUnit * D / 2, kPacked = kCodes + kChunkUnits * 64 * NG;
   static constexpr int kRing = EXACT && D == 128 ? 4 : 8;  // what shared memory leaves
   static constexpr size_t kControl = 1024;
-  static constexpr size_t kSmem = kControl + 2 * kBuf + kRing * kPacked;
+  static constexpr size_t kSmem = kControl + 2 * kBuf + 2 * kRing * kPacked;
   // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
   static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
 
 struct Control {
-  uint64_t ring_full[8], ring_empty[8];
-  uint64_t k_full[2], v_full[2], pv_done[2], s_full[2], p_full[2], q_full, pair[4];
+  uint64_t ring_full[2][8], ring_empty[2][8];  // keys, values
+  uint64_t k_full[2], v_full[2], pv_done[2], s_full[2], p_full[2], q_full;
   uint32_t tmem;
   int gave_up;
-  int gone[8];  // units of the last eight tiles that are not there (bits)
+  int gone[2][8];  // units of the last eight tiles that are not there (bits), by each loader
   int64_t sums[kWarps];
   int start_b;
   int64_t start_in;
 };
 static_assert(sizeof(Control) <= 1024, "in front of the operands");
 
-// A bounded wait that all of the block gives up together.
+// A bounded wait that the whole block gives up together: from then on every wait returns at once, the
+// loader and the mma thread stop, and the other roles run to their end on whatever is there.
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
     if (ptx::mbar_try(bar, parity & 1)) return true;
-    if ((i & 63) == 63 && *(volatile int*)&c->gave_up) return false;
+    if ((i & 15) == 15 && *(volatile int*)&c->gave_up) return false;
   }
   *(volatile int*)&c->gave_up = 1;
   return false;
 }
+// Warps that wait for an mbarrier are woken, and poll, whenever any mbarrier of the block moves: with all
+// 31 of them doing so half of the issued instructions were polls.  So one warp of a group waits, and the
+// others for it at a named barrier.
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+enum { kBarSoftmax = 1, kBarQuad = 2, kBarKeys = 6, kBarValues = 8 };
 
 // The items of a block's range of the line, one at a time, the same in every role.
 template <int D>
@@ -143,12 +152,12 @@ __device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) {
 // words) of a token.  Rows go K-major with the 128-byte swizzle; lanes are spread so that no eight of
 // them meet in a bank.
 template <int D, int G, bool EXACT>
-__device__ __forceinline__ void unpack_keys(uint32_t unit, uint32_t buf, int place, int ch, int row_unit) {
+__device__ __forceinline__ void unpack_keys(uint32_t codes_at, uint32_t scales_at, uint32_t buf, int place, int ch, int row_unit) {
   using C = Shape<D, G, EXACT>;
   uint32_t w[4], sc[C::NG];
   // packed row `place` holds token 0 4 1 5 2 6 3 7 (+ 8)
-  lds<16>(unit + place * (D / 2) + ch * 16, w);
-  lds<4 * C::NG>(unit + off_ks(D) + place * 4 * C::NG, sc);
+  lds<16>(codes_at + place * (D / 2) + ch * 16, w);
+  lds<4 * C::NG>(scales_at + place * 4 * C::NG, sc);
   const int n = row_unit + (place >> 1 & 3) + 4 * (place & 1) + (place & 8);
   const uint32_t krow = buf + n * 128;
 #pragma unroll
@@ -180,12 +189,12 @@ __device__ __forceinline__ void unpack_keys(uint32_t unit, uint32_t buf, int pla
 
 // The same of values: rows go MN-major.  seen: somebody sees the token; its values are 0 otherwise.
 template <int D, int G, bool EXACT>
-__device__ __forceinline__ void unpack_values(uint32_t unit, uint32_t buf, int place, int ch, int row, bool seen) {
+__device__ __forceinline__ void unpack_values(uint32_t codes_at, uint32_t scales_at, uint32_t buf, int place, int ch, int row, bool seen) {
   using C = Shape<D, G, EXACT>;
   uint32_t w[4], sz;
-  lds<16>(unit + off_v(D) + place * (D / 2) + ch * 16, w);
+  lds<16>(codes_at + place * (D / 2) + ch * 16, w);
   const int group = D == 128 ? ch ^ (place & 2) : ch;  // 32 coordinates
-  lds<4>(unit + off_vs(D, G) + (place * C::NG + group * 32 / G) * 4, &sz);
+  lds<4>(scales_at + (place * C::NG + group * 32 / G) * 4, &sz);
   if (!seen) sz = 0;
   if (D == 128 && (group & 2)) {
     uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
@@ -211,7 +220,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   using C = Shape<D, G, kExact>;
   constexpr int kRing = C::kRing;
   extern __shared__ __align__(1024) uint8_t raw_smem[];
-  __shared__ float row_max[2][2][kRows];  // [tile's parity][half of the columns]
+  __shared__ float shared_rows[2][4][kRows];  // numbers that the four threads of a row give each other
   Control& ctl = *reinterpret_cast<Control*>(raw_smem);
   uint8_t* smem = raw_smem + C::kControl;
   uint8_t* packed = smem + 2 * C::kBuf;
@@ -221,8 +230,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   if (tid == 0) {
     ctl.gave_up = 0;
     for (int i = 0; i < kRing; ++i) {
-      ptx::mbar_init(&ctl.ring_full[i], C::kChunkUnits);
-      ptx::mbar_init(&ctl.ring_empty[i], kUnpackWarps);
+      for (int k = 0; k < 2; ++k) {
+        ptx::mbar_init(&ctl.ring_full[k][i], C::kChunkUnits);
+        ptx::mbar_init(&ctl.ring_empty[k][i], 4);  // every other chunk's keys are the other four warps'
+      }
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&ctl.k_full[i], kKeyWarps);
@@ -232,7 +243,6 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       ptx::mbar_init(&ctl.p_full[i], kSoftmaxWarps);
     }
     ptx::mbar_init(&ctl.q_full, 4);
-    for (int i = 0; i < 4; ++i) ptx::mbar_init(&ctl.pair[i], 2);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -308,23 +318,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     // ---------------------------------------------------------------- softmax
     RowsPart<D>* out_part = reinterpret_cast<RowsPart<D>*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int half = warp >> 2, my_row = tid & (kRows - 1);
+    const int quarter = warp >> 2, my_row = tid & (kRows - 1);
     int left_part[2] = {0, 0};
-    uint32_t meets = 0;  // of the two warps that share rows
-    bool ok = true;
-    // gives the other warp a number per row and takes its own; both see all that was done before
-    const auto swap = [&](float x, float& y) {
-      row_max[meets & 1][half][my_row] = x;
+    uint32_t meets = 0;  // of the four warps that share rows
+    // Gives the other threads of the row a number and waits for theirs; all see what was done before.
+    const auto meet = [&](float x) {
+      shared_rows[meets & 1][quarter][my_row] = x;
       ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&ctl.pair[warp & 3]);
-      const bool met = __all_sync(~0u, wait(&ctl, &ctl.pair[warp & 3], meets));
+      named_sync(kBarQuad + (warp & 3), 128);
       ptx::tc_fence_after();
-      if (met) y = row_max[meets & 1][half ^ 1][my_row];
       ++meets;
-      return met;
     };
-    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+    const auto theirs = [&](int i) { return shared_rows[(meets - 1) & 1][i][my_row]; };
+    // the whole role waits for an mbarrier
+    const auto all_wait = [&](uint64_t* bar, uint32_t parity) {
+      if (warp == 0) wait(&ctl, bar, parity);
+      named_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      ptx::tc_fence_after();
+    };
+    for (bool begun = false; it.next(a, r, begun); begun = true) {
       const uint32_t row = it.rb * kRows + my_row;
       const bool in = row < (uint32_t)it.s.rows;
       const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
@@ -363,7 +375,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           down = -down;
         }
         kappa = fmaxf(kappa, 1e-37f);  // so that -inf, a masked score, stays that
-        if (half == 0) {
+        if (quarter == 0) {
           float sum[C::NG];
 #pragma unroll
           for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
@@ -412,41 +424,37 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
 
         for (int j = it.t0; j < it.t1; ++j, ++tile) {
           const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf;
-          ok = __all_sync(~0u, wait(&ctl, &ctl.s_full[buf], tile >> 1));
-          if (!ok) break;
-          ptx::tc_fence_after();
-          uint32_t sr[64];
-          ptx::tmem_ld_cols<0, 64>(sp + 64 * half, sr);
+          all_wait(&ctl.s_full[buf], tile >> 1);
+          uint32_t sr[32];
+          ptx::tmem_ld_cols<0, 32>(sp + 32 * quarter, sr);
           ptx::tmem_wait_ld();
-          const int pos0 = it.base_u * kUnit + j * kTile + 64 * half;
+          const int pos0 = it.base_u * kUnit + j * kTile + 32 * quarter;
           // what this row sees of these columns: [c0, c1), less units that are not there
-          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[tile & 7] >> (4 * half) & 15;
-          if (__any_sync(~0u, c0 > 0 || c1 < 64 || gone != 0)) {
+          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[0][tile & 7] >> (2 * quarter) & 3;
+          if (__any_sync(~0u, c0 > 0 || c1 < 32 || gone != 0)) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
+            for (int c = 0; c < 32; ++c)
               if (c < c0 || c >= c1 || (gone >> (c / kUnit) & 1)) sr[c] = 0xFF800000u;
           }
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 64; c += 8)
+          for (int c = 0; c < 32; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(sr[c + i])), __uint_as_float(sr[c + 4 + i]));
-          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])) * kappa, other = 0.f;
-          ok = swap(top, other);  // both halves of S are in registers now: P may take its place
-          if (!ok) break;
-          top = fmaxf(top, other);
+          meet(fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])));  // all of S is in registers now: P may take its place
+          const float top = fmaxf(fmaxf(theirs(0), theirs(1)), fmaxf(theirs(2), theirs(3))) * kappa;
           if (__any_sync(~0u, top > m + 8.f)) {
             const float now = fmaxf(m, top), f = ex2(m - now);
             m = now;
             l *= f;
             if (j > it.t0) {
-              // O is the softmax's once the tile before is in it; each warp takes half of the columns
-              ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1));
-              if (!ok) break;
+              // O is the softmax's once the tile before is in it; each warp takes a quarter of the columns
+              wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1);
+              __syncwarp();
               ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+              for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
                 uint32_t o[16];
                 ptx::tmem_ld16(lanes + C::O + c, o);
                 ptx::tmem_wait_ld();
@@ -459,10 +467,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           }
           float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint32_t p[16], pl[16];
+          for (int c = 0; c < 32; c += 16) {
+            uint32_t p[8], pl[8];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < 8; ++i) {
               const float s0 = __uint_as_float(sr[c + 2 * i]), s1 = __uint_as_float(sr[c + 2 * i + 1]);
               const float x = ex2(fmaf(s0, kappa, -m)), y = ex2(fmaf(s1, kappa, -m));
               sum4[i & 3] += x + y;
@@ -473,8 +481,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                 pl[i] = u32(__floats2half2_rn(x - back.x, y - back.y));
               }
             }
-            ptx::tmem_st16(sp + 32 * half + c / 2, p);
-            if (kExact) ptx::tmem_st16(sp + 64 + 32 * half + c / 2, pl);
+            ptx::tmem_st8(sp + 16 * quarter + c / 2, p);
+            if (kExact) ptx::tmem_st8(sp + 64 + 16 * quarter + c / 2, pl);
           }
           l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
           ptx::tmem_wait_st();
@@ -482,11 +490,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl.p_full[buf]);
         }
-        if (!ok) break;
-        float other = 0.f;
-        ok = __all_sync(~0u, wait(&ctl, &ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1)) && swap(l, other);
-        if (!ok) break;
-        l += other;
+        all_wait(&ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1);
+        meet(l);
+        l = (theirs(0) + theirs(1)) + (theirs(2) + theirs(3));
         ptx::tc_fence_after();
       }
       const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.s.cost;
@@ -495,7 +501,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
       T* dst = static_cast<T*>(a.out) + ((int64_t)(it.s.q0 + tok) * a.hq + it.head * r + hh) * D;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+      for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
         uint32_t o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0;
@@ -519,18 +525,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         }
       }
       if (!whole) {
-        if (in && half == 0) {
+        if (in && quarter == 0) {
           part->m[my_row] = m;
           part->l[my_row] = l;
         }
         left_part[k] = 1;
         if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{it.to == it.s.cost ? 3 : 1, it.s.q0, it.s.rows, it.head, it.rb};
       }
-      // O is read before the next item's first product: its q comes after both warps met here
-      if (any) {
-        float none;
-        ok = swap(0.f, none);
-      }
+      // O is read before the next item's first product: its q comes after the warps met here
+      if (any) meet(0.f);
     }
     if (tid == 0)
       for (int k = 0; k < 2; ++k)
@@ -540,36 +543,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     constexpr int kStep = 1024 / D;  // tokens of a warp's step
     const bool keys = warp < kSoftmaxWarps + kKeyWarps;
     const int ch = lane % (D / 32), row_lane = lane / (D / 32);
+    const bool leads = (warp & 3) == 0;
+    const int group = warp >> 2 & 1;  // of the keys' warps: they take every other chunk
     uint32_t chunk = 0;
-    bool ok = true;
-    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
-      for (int j = it.t0; j < it.t1 && ok; ++j, ++tile) {
+    for (bool begun = false; it.next(a, r, begun); begun = true) {
+      for (int j = it.t0; j < it.t1; ++j, ++tile) {
         const uint32_t buf = tile & 1, base = smem32 + buf * C::kBuf;
         // keys are done with when their scores are, values when the products with the weights are
-        if (tile >= 2) ok = __all_sync(~0u, wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1));
-        for (int c = 0; c < C::kChunks && ok; ++c, ++chunk) {
+        if (leads && tile >= 2) wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1);
+        for (int c = 0; c < C::kChunks; ++c, ++chunk) {
           const uint32_t slot = chunk % kRing;
-          ok = __all_sync(~0u, wait(&ctl, &ctl.ring_full[slot], chunk / kRing));
-          if (!ok) break;
-          const uint32_t units = packed32 + slot * C::kPacked;
-          const int row0 = c * C::kChunkUnits * kUnit;  // of the tile
+          if (keys && group != (c & 1)) continue;  // the other four warps' chunk
+          if (leads) wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
+          named_sync(keys ? kBarKeys + group : kBarValues, 128);
+          const uint32_t at = packed32 + ((keys ? 0 : kRing) + slot) * C::kPacked;
+          const int row0 = c * C::kChunkUnits * kUnit, in_chunk = (warp & 3) * kStep + row_lane, row = row0 + in_chunk;  // of the tile
+          const uint32_t codes_at = at + in_chunk / kUnit * (kUnit * D / 2), scales_at = at + C::kCodes + in_chunk / kUnit * (64 * C::NG);
           if (keys) {
-            const int row = (warp - kSoftmaxWarps) * kStep + row_lane;
-            unpack_keys<D, G, kExact>(units + row / kUnit * C::UB, base, row % kUnit, ch, row0 + (row & ~(kUnit - 1)));
+            unpack_keys<D, G, kExact>(codes_at, scales_at, base, row % kUnit, ch, row & ~(kUnit - 1));
           } else {
-            const int gone = *(volatile int*)&ctl.gone[tile & 7];
-#pragma unroll
-            for (int i = 0; i < kKeyWarps / kValueWarps; ++i) {
-              const int row = ((warp - kSoftmaxWarps - kKeyWarps) * (kKeyWarps / kValueWarps) + i) * kStep + row_lane;
-              const int pos = it.base_u * kUnit + j * kTile + row0 + row;
-              unpack_values<D, G, kExact>(units + row / kUnit * C::UB, base + C::kK, row % kUnit, ch, row0 + row,
-                                          pos >= it.first && pos < it.end && !(gone >> ((row0 + row) / kUnit) & 1));
-            }
+            const int pos = it.base_u * kUnit + j * kTile + row, gone = *(volatile int*)&ctl.gone[1][tile & 7];
+            unpack_values<D, G, kExact>(codes_at, scales_at, base + C::kK, row % kUnit, ch, row,
+                                        pos >= it.first && pos < it.end && !(gone >> (row / kUnit) & 1));
           }
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl.ring_empty[slot]);
+          if (lane == 0) ptx::mbar_arrive(&ctl.ring_empty[!keys][slot]);
         }
-        if (!ok) break;
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(keys ? &ctl.k_full[buf] : &ctl.v_full[buf]);
@@ -627,7 +626,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       ++item;
     }
   } else {
-    // ---------------------------------------------------------------- loader
+    // ---------------------------------------------------------------- loaders
+    const int kind = warp - (kSoftmaxWarps + kUnpackWarps + 1);  // keys, values
     bool ok = true;
     const int shift = page_shift - 4;
     uint32_t chunk = 0;
@@ -644,23 +644,27 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           id_next = entry(u_begin + j * C::kChunkUnits + 32 + lane);
         }
         const uint32_t slot = chunk % kRing;
-        if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[slot], chunk / kRing - 1));
+        if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[kind][slot], chunk / kRing - 1));
         if (!ok) break;
         const bool good = id >= 0 && id < a.n_blocks;
         const uint32_t there = __ballot_sync(~0u, good) >> (at & ~(kTileUnits - 1));
-        // A tile's first chunk brings its mask.  The place is free: values of a tile at most four back are
-        // being unpacked, so the products of one six back are done and the softmax is past the one eight back.
-        if (j % C::kChunks == 0 && lane == at) *(volatile int*)&ctl.gone[(chunk / C::kChunks) & 7] = ~there & ((1 << kTileUnits) - 1);
+        // A tile's first chunk brings its mask.  The place is free: a ring holds two tiles at most, the keys
+        // of the tile two back are unpacked when the scores of the one four back are done, these come after
+        // the weights of the one six back, and the softmax is past the one eight back.
+        if (j % C::kChunks == 0 && lane == at) *(volatile int*)&ctl.gone[kind][(chunk / C::kChunks) & 7] = ~there & ((1 << kTileUnits) - 1);
         __syncwarp();
         const int i = lane - at;
         if ((unsigned)i < C::kChunkUnits) {
           if (good) {
             const int u = u_begin + j * C::kChunkUnits + i;
             const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
-            ptx::mbar_arrive_expect_tx(&ctl.ring_full[slot], C::UB);
-            ptx::bulk_load(packed + slot * C::kPacked + i * C::UB, src, C::UB, &ctl.ring_full[slot]);
+            uint8_t* dst = packed + (kind * kRing + slot) * C::kPacked;
+            constexpr int kCodes = kUnit * D / 2, kScales = 64 * C::NG;
+            ptx::mbar_arrive_expect_tx(&ctl.ring_full[kind][slot], kCodes + kScales);
+            ptx::bulk_load(dst + i * kCodes, src + kind * kCodes, kCodes, &ctl.ring_full[kind][slot]);
+            ptx::bulk_load(dst + C::kCodes + i * kScales, src + 2 * kCodes + kind * kScales, kScales, &ctl.ring_full[kind][slot]);
           } else {
-            ptx::mbar_arrive(&ctl.ring_full[slot]);
+            ptx::mbar_arrive(&ctl.ring_full[kind][slot]);
           }
         }
         __syncwarp();
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     }
     // copies in flight land before the block ends, also where a wait gave up
     if (!ok)
-      for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[t % kRing], (t / kRing) & 1);
+      for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[kind][t % kRing], (t / kRing) & 1);
   }
 
   ptx::tc_fence_before();
@@ -724,7 +728,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(AttnArgs a) {
 template <typename T, int D, int G>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   constexpr size_t bytes = Shape<D, G, __is_same(T, __half)>::kSmem;
-  static_assert(bytes + 4 * 2 * 2 * kRows <= 227 * 1024, "shared memory of a block");
+  static_assert(bytes + 4 * 2 * 4 * kRows <= 227 * 1024, "shared memory of a block");
   static_assert(sizeof(RowsPart<D>) % 16 == 0, "parts are read in 16 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
