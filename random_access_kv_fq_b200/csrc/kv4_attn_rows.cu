@@ -3,11 +3,10 @@
 //
 // One block per SM, its warps in roles that meet in mbarriers, over tiles of 128 tokens:
 //   loaders  copy the units' keys and their values (bulk copies) into a ring each of packed cache;
-//   unpack   8 warps turn keys and 4 turn values into fp16 operands in shared memory, two tiles deep;
+//   unpack   4 warps turn keys and 4 turn values into fp16 operands in shared memory, two tiles deep;
 //   mma      one thread issues tcgen05.mma: S = Q K^T into one of two buffers of tensor memory,
 //            O += P V with P in tensor memory, the next tile's S under this tile's softmax;
-//   softmax  16 warps, four threads to a row: S out of tensor memory, weights P back into its place.
-// All of them run one long chain of short instructions each, so there are as many as 64 registers allow.
+//   softmax  8 warps, two threads to a row: S out of tensor memory, weights P back into its place.
 // q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), half a step (2^-12) off.
 // For bf16 outputs, whose own rounding is 2^-9, keys and weights are fp16 numbers likewise.  For fp16
 // outputs neither may add to it:  s is split into its leading 7 bits and the rest, so that s_hi c and
@@ -35,9 +34,11 @@ constexpr int kRows = 128;      // rows of a block's item
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kTileUnits = kTile / kUnit;
 constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
-constexpr int kSoftmaxWarps = 16;  // warps w, w + 4, .. share 32 rows, 32 columns each
-constexpr int kKeyWarps = 8, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueWarps;
-constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 3;
+constexpr int kSoftmaxWarps = 8;  // warps w and w + 4 share 32 rows, 64 columns each
+constexpr int kKeyWarps = 4, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueWarps;
+constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 4;  // mma, two loaders, one idle: whole warpgroups
+// registers a thread: 96 at launch, 20 warps x 96 = 8 x 144 + 12 x 64
+constexpr int kSoftmaxRegs = 144, kOtherRegs = 64;
 
 template <int D>
 struct RowsPart {
@@ -88,7 +89,7 @@ __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity)
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-enum { kBarSoftmax = 1, kBarQuad = 2, kBarKeys = 6, kBarValues = 8 };
+enum { kBarSoftmax = 1, kBarPair = 2, kBarKeys = 6, kBarValues = 7 };
 
 // The items of a block's range of the line, one at a time, the same in every role.
 template <int D>
@@ -220,7 +221,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   using C = Shape<D, G, kExact>;
   constexpr int kRing = C::kRing;
   extern __shared__ __align__(1024) uint8_t raw_smem[];
-  __shared__ float shared_rows[2][4][kRows];  // numbers that the four threads of a row give each other
+  __shared__ float shared_rows[2][2][kRows];  // numbers that the two threads of a row give each other
   Control& ctl = *reinterpret_cast<Control*>(raw_smem);
   uint8_t* smem = raw_smem + C::kControl;
   uint8_t* packed = smem + 2 * C::kBuf;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     for (int i = 0; i < kRing; ++i) {
       for (int k = 0; k < 2; ++k) {
         ptx::mbar_init(&ctl.ring_full[k][i], C::kChunkUnits);
-        ptx::mbar_init(&ctl.ring_empty[k][i], 4);  // every other chunk's keys are the other four warps'
+        ptx::mbar_init(&ctl.ring_empty[k][i], 4);
       }
     }
     for (int i = 0; i < 2; ++i) {
@@ -315,21 +316,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
 
   if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
     // ---------------------------------------------------------------- softmax
     RowsPart<D>* out_part = reinterpret_cast<RowsPart<D>*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
     const uint32_t lanes = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const int quarter = warp >> 2, my_row = tid & (kRows - 1);
+    const int half = warp >> 2, my_row = tid & (kRows - 1);
     int left_part[2] = {0, 0};
-    uint32_t meets = 0;  // of the four warps that share rows
-    // Gives the other threads of the row a number and waits for theirs; all see what was done before.
+    uint32_t meets = 0;  // of the two warps that share rows
+    // Gives the row's other thread a number and waits for its; both see what was done before.
     const auto meet = [&](float x) {
-      shared_rows[meets & 1][quarter][my_row] = x;
+      shared_rows[meets & 1][half][my_row] = x;
       ptx::tc_fence_before();
-      named_sync(kBarQuad + (warp & 3), 128);
+      named_sync(kBarPair + (warp & 3), 64);
       ptx::tc_fence_after();
       ++meets;
     };
-    const auto theirs = [&](int i) { return shared_rows[(meets - 1) & 1][i][my_row]; };
+    const auto theirs = [&] { return shared_rows[(meets - 1) & 1][half ^ 1][my_row]; };
     // the whole role waits for an mbarrier
     const auto all_wait = [&](uint64_t* bar, uint32_t parity) {
       if (warp == 0) wait(&ctl, bar, parity);
@@ -375,7 +377,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           down = -down;
         }
         kappa = fmaxf(kappa, 1e-37f);  // so that -inf, a masked score, stays that
-        if (quarter == 0) {
+        if (half == 0) {
           float sum[C::NG];
 #pragma unroll
           for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
@@ -425,36 +427,37 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         for (int j = it.t0; j < it.t1; ++j, ++tile) {
           const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf;
           all_wait(&ctl.s_full[buf], tile >> 1);
-          uint32_t sr[32];
-          ptx::tmem_ld_cols<0, 32>(sp + 32 * quarter, sr);
+          uint32_t sr[64];
+          ptx::tmem_ld_cols<0, 64>(sp + 64 * half, sr);
           ptx::tmem_wait_ld();
-          const int pos0 = it.base_u * kUnit + j * kTile + 32 * quarter;
+          const int pos0 = it.base_u * kUnit + j * kTile + 64 * half;
           // what this row sees of these columns: [c0, c1), less units that are not there
-          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[0][tile & 7] >> (2 * quarter) & 3;
-          if (__any_sync(~0u, c0 > 0 || c1 < 32 || gone != 0)) {
+          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[0][tile & 7] >> (4 * half) & 15;
+          if (__any_sync(~0u, c0 > 0 || c1 < 64 || gone != 0)) {
 #pragma unroll
-            for (int c = 0; c < 32; ++c)
+            for (int c = 0; c < 64; ++c)
               if (c < c0 || c >= c1 || (gone >> (c / kUnit) & 1)) sr[c] = 0xFF800000u;
           }
           float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int c = 0; c < 32; c += 8)
+          for (int c = 0; c < 64; c += 8)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(sr[c + i])), __uint_as_float(sr[c + 4 + i]));
-          meet(fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3])));  // all of S is in registers now: P may take its place
-          const float top = fmaxf(fmaxf(theirs(0), theirs(1)), fmaxf(theirs(2), theirs(3))) * kappa;
+          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
+          meet(top);  // all of S is in registers now: P may take its place
+          top = fmaxf(top, theirs()) * kappa;
           if (__any_sync(~0u, top > m + 8.f)) {
             const float now = fmaxf(m, top), f = ex2(m - now);
             m = now;
             l *= f;
             if (j > it.t0) {
-              // O is the softmax's once the tile before is in it; each warp takes a quarter of the columns
+              // O is the softmax's once the tile before is in it; each warp takes half of the columns
               wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1);
               __syncwarp();
               ptx::tc_fence_after();
 #pragma unroll 1
-              for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+              for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                 uint32_t o[16];
                 ptx::tmem_ld16(lanes + C::O + c, o);
                 ptx::tmem_wait_ld();
@@ -467,10 +470,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           }
           float sum4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int c = 0; c < 32; c += 16) {
-            uint32_t p[8], pl[8];
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t p[16], pl[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < 16; ++i) {
               const float s0 = __uint_as_float(sr[c + 2 * i]), s1 = __uint_as_float(sr[c + 2 * i + 1]);
               const float x = ex2(fmaf(s0, kappa, -m)), y = ex2(fmaf(s1, kappa, -m));
               sum4[i & 3] += x + y;
@@ -481,8 +484,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                 pl[i] = u32(__floats2half2_rn(x - back.x, y - back.y));
               }
             }
-            ptx::tmem_st8(sp + 16 * quarter + c / 2, p);
-            if (kExact) ptx::tmem_st8(sp + 64 + 16 * quarter + c / 2, pl);
+            ptx::tmem_st16(sp + 32 * half + c / 2, p);
+            if (kExact) ptx::tmem_st16(sp + 64 + 32 * half + c / 2, pl);
           }
           l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
           ptx::tmem_wait_st();
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         }
         all_wait(&ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1);
         meet(l);
-        l = (theirs(0) + theirs(1)) + (theirs(2) + theirs(3));
+        l += theirs();
         ptx::tc_fence_after();
       }
       const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.s.cost;
@@ -501,7 +504,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
       T* dst = static_cast<T*>(a.out) + ((int64_t)(it.s.q0 + tok) * a.hq + it.head * r + hh) * D;
 #pragma unroll 1
-      for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 16) {
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
         uint32_t o[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[i] = 0;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         }
       }
       if (!whole) {
-        if (in && quarter == 0) {
+        if (in && half == 0) {
           part->m[my_row] = m;
           part->l[my_row] = l;
         }
@@ -539,12 +542,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       for (int k = 0; k < 2; ++k)
         if (!left_part[k]) out_hdr[blockIdx.x * 2 + k].state = 0;
   } else if (warp < kSoftmaxWarps + kUnpackWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     // ---------------------------------------------------------------- unpack
     constexpr int kStep = 1024 / D;  // tokens of a warp's step
     const bool keys = warp < kSoftmaxWarps + kKeyWarps;
     const int ch = lane % (D / 32), row_lane = lane / (D / 32);
     const bool leads = (warp & 3) == 0;
-    const int group = warp >> 2 & 1;  // of the keys' warps: they take every other chunk
     uint32_t chunk = 0;
     for (bool begun = false; it.next(a, r, begun); begun = true) {
       for (int j = it.t0; j < it.t1; ++j, ++tile) {
@@ -553,9 +556,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         if (leads && tile >= 2) wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1);
         for (int c = 0; c < C::kChunks; ++c, ++chunk) {
           const uint32_t slot = chunk % kRing;
-          if (keys && group != (c & 1)) continue;  // the other four warps' chunk
           if (leads) wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
-          named_sync(keys ? kBarKeys + group : kBarValues, 128);
+          named_sync(keys ? kBarKeys : kBarValues, 128);
           const uint32_t at = packed32 + ((keys ? 0 : kRing) + slot) * C::kPacked;
           const int row0 = c * C::kChunkUnits * kUnit, in_chunk = (warp & 3) * kStep + row_lane, row = row0 + in_chunk;  // of the tile
           const uint32_t codes_at = at + in_chunk / kUnit * (kUnit * D / 2), scales_at = at + C::kCodes + in_chunk / kUnit * (64 * C::NG);
@@ -574,7 +576,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         if (lane == 0) ptx::mbar_arrive(keys ? &ctl.k_full[buf] : &ctl.v_full[buf]);
       }
     }
-  } else if (warp == kSoftmaxWarps + kUnpackWarps) {
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    if (warp == kSoftmaxWarps + kUnpackWarps) {
     // ---------------------------------------------------------------- mma
     constexpr uint32_t idesc_s = ptx::idesc_f16_f32(128, kTile), idesc_o = ptx::idesc_f16_f32(128, D) | (1u << 16);
     bool ok = true;
@@ -625,7 +629,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       tile += it.t1 - it.t0;
       ++item;
     }
-  } else {
+    } else if (warp < kSoftmaxWarps + kUnpackWarps + 3) {
     // ---------------------------------------------------------------- loaders
     const int kind = warp - (kSoftmaxWarps + kUnpackWarps + 1);  // keys, values
     bool ok = true;
@@ -673,6 +677,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     // copies in flight land before the block ends, also where a wait gave up
     if (!ok)
       for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[kind][t % kRing], (t / kRing) & 1);
+    }
   }
 
   ptx::tc_fence_before();
@@ -728,7 +733,7 @@ __global__ void __launch_bounds__(128) rows_join_kernel(AttnArgs a) {
 template <typename T, int D, int G>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   constexpr size_t bytes = Shape<D, G, __is_same(T, __half)>::kSmem;
-  static_assert(bytes + 4 * 2 * 4 * kRows <= 227 * 1024, "shared memory of a block");
+  static_assert(bytes + 4 * 2 * 2 * kRows <= 227 * 1024, "shared memory of a block");
   static_assert(sizeof(RowsPart<D>) % 16 == 0, "parts are read in 16 bytes");
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
