@@ -397,9 +397,9 @@ fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, i
                        int64_t n_blocks, int page, int group, void* k_values, void* v_values,
                        void* stream);
 
-/* Workspace bytes of fq_kv4_attn for these sizes, or 0 when they are unsupported.  The value depends
- * on nothing else: not on the number of sequences, nor on their lengths. */
-size_t fq_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q);
+/* Workspace bytes that fq_kv4_attn needs for these sizes: 0 where no item is split (few sequences and
+ * short tables) and when they are unsupported.  The value depends only on the arguments. */
+size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int max_blocks, int page);
 
 /*
  * fq_kv4_attn - causal attention of one or more query tokens per sequence over the 4-bit cache:
@@ -416,8 +416,9 @@ size_t fq_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q);
  *             may hold anything.
  *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
  *             sequence has are left as they were.
- *   workspace fq_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q) bytes, 16-byte aligned, owned by the caller and
- *             overwritten; calls that may overlap (two streams, two captured graphs) need one each.
+ *   workspace fq_kv4_attn_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0), owned by the
+ *             caller and overwritten; calls that may overlap (two streams, two captured graphs) need
+ *             one each.
  * Precondition: the groups of tokens that are seen span less than 65504 (15 s and c s + z are fp16
  * numbers on the way).
  * B <= 8192, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.

@@ -71,7 +71,7 @@ _SIGS = {
                           _vp]),
     "fq_kv4_write": (_i, [_vp, _vp, _i, _c_i64, _i, _i, _c_i64, _c_i64, _c_i64, _c_i64, _vp, _vp,
                           _c_i64, _i, _i, _vp, _vp, _vp]),
-    "fq_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "fq_kv4_attn_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "fq_kv4_attn": (_i, [_vp, _i, _c_i64, _i, _i, _c_i64, _c_i64, _vp, _i, _i, _vp, _c_i64, _i, _i,
                          _i, _vp, _i, _vp, _i, ctypes.c_float, _vp, _vp, _sz, _vp]),
 }
@@ -380,21 +380,37 @@ def fq_build_search_index(codebook, d: int, k: int, N: int, kind: int, L: int,
 
 # ---- the 4-bit paged cache ---------------------------------------------------------------------
 
-# These calls take microseconds of GPU time, so the checks below are kept to cheap attribute reads.
+# These calls take microseconds of GPU time, so the checks below are kept to cheap attribute reads and
+# the common case (the current device's current stream) goes straight through.
 
-_KV4_UNITS = {}   # (d, group) -> unit bytes
-_KV4_WS = {}      # (Hq, Hkv, d, max_q) -> workspace bytes
+class _Torch:
+    """What the calls below need of torch, looked up once."""
+
+    def __init__(self):
+        import torch
+        self.device, self.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.int32, self.uint8 = torch.int32, torch.uint8
+        self.types = {torch.float16: FQ_F16, torch.float32: FQ_F32, torch.bfloat16: FQ_BF16}
 
 
-def _device_index(*tensors) -> int:
-    """The index of the CUDA device that all tensors (None among them is skipped) are on."""
-    dev = tensors[0].get_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors on different devices")
-    if dev < 0:
-        raise ValueError("expected CUDA tensors")
-    return dev
+_torch = None
+_KV4_SIZES = {}  # arguments of the size functions -> bytes
+
+
+def _t() -> _Torch:
+    global _torch
+    if _torch is None:
+        _torch = _Torch()
+    return _torch
+
+
+def _kv4_size(fn, *args) -> int:
+    n = _KV4_SIZES.get((fn, args))
+    if n is None:
+        if len(_KV4_SIZES) > 4096:
+            _KV4_SIZES.clear()
+        n = _KV4_SIZES[fn, args] = int(getattr(lib(), fn)(*args))
+    return n
 
 
 class _OnStream:
@@ -403,6 +419,8 @@ class _OnStream:
 
     def __init__(self, device: int, stream):
         import torch
+        if device < 0:
+            raise ValueError("expected CUDA tensors")
         if stream is None:
             stream = torch.cuda.current_stream(device)
         elif isinstance(stream, int):
@@ -420,34 +438,34 @@ class _OnStream:
         return self._ctx.__exit__(*exc)
 
 
-def _raw_stream(device: int) -> Optional[int]:
-    """The raw current stream of `device`, or None when another device is current."""
-    import torch
-    if torch._C._cuda_getDevice() != device:
-        return None
-    return torch._C._cuda_getCurrentRawStream(device)
+def _same_device(device: int, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError("tensors on different devices")
 
 
 def _int32(name, t, shape):
-    import torch
-    if t.dtype is not torch.int32 or not t.is_contiguous():
+    if t.dtype is not _torch.int32 or not t.is_contiguous():
         raise TypeError(f"{name}: a contiguous int32 tensor")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _kv4_type(t) -> int:
+    code = _torch.types.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
+
+
 def _kv4_cache(cache, d: int, group: int):
     """(n_blocks, Hkv, page) of a cache tensor [n_blocks, Hkv, page / 16, unit bytes]."""
-    import torch
-    if cache.dtype is not torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
+    if cache.dtype is not _torch.uint8 or not cache.is_contiguous():
         raise TypeError("cache: a contiguous uint8 tensor [n_blocks, Hkv, page / 16, unit bytes]")
-    unit = _KV4_UNITS.get((d, group))
-    if unit is None:
-        unit = fq_kv4_unit_bytes(d, group)
-        if unit == 0:
-            raise FQError("fq_kv4_unit_bytes", 2)
-        _KV4_UNITS[d, group] = unit
     n_blocks, hkv, units, size = cache.shape
+    unit = _kv4_size("fq_kv4_unit_bytes", d, group)
+    if unit == 0:
+        raise FQError("fq_kv4_unit_bytes", 2)
     if size != unit:
         raise ValueError(f"cache: units of {size} bytes, expected {unit}")
     return n_blocks, hkv, 16 * units
@@ -457,8 +475,9 @@ def fq_kv4_unit_bytes(d: int, group: int) -> int:
     return int(lib().fq_kv4_unit_bytes(d, group))
 
 
-def fq_kv4_attn_workspace_bytes(Hq: int, Hkv: int, d: int, max_q: int) -> int:
-    return int(lib().fq_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q))
+def fq_kv4_attn_workspace_bytes(B: int, Hq: int, Hkv: int, d: int, max_q: int, max_blocks: int,
+                                page: int) -> int:
+    return int(lib().fq_kv4_attn_workspace_bytes(B, Hq, Hkv, d, max_q, max_blocks, page))
 
 
 def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int, n_slots: int,
@@ -467,29 +486,26 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
     add new_lens [B] (negative: end) and grow block_tables [B, max_blocks] from the stack
     free_list[:free_count]; tables and free list are updated in place, free_count too unless
     free_count_out is given.  Returns (lens_out [B], cu_new [B + 1], slots [n_slots], refused [1])."""
-    dev = _device_index(lens, new_lens, block_tables, free_list, free_count, lens_out,
-                        free_count_out)
-    raw = _raw_stream(dev) if stream is None else None
-    if raw is None:
+    tt = _t()
+    dev = lens.get_device()
+    _same_device(dev, new_lens, block_tables, free_list, free_count, lens_out, free_count_out)
+    if stream is not None or dev < 0 or tt.device() != dev:
         with _OnStream(dev, stream):
             return fq_page_step(lens, new_lens, block_tables, free_list, free_count, page, n_slots,
                                 lens_out, free_count_out)
-    B = lens.numel()
+    B, max_blocks = block_tables.shape
+    n_blocks = free_list.numel()
     _int32("lens", lens, (B,))
     _int32("new_lens", new_lens, (B,))
-    if block_tables.dim() != 2:
-        raise ValueError("block_tables: [B, max_blocks]")
-    max_blocks = block_tables.shape[1]
     _int32("block_tables", block_tables, (B, max_blocks))
-    n_blocks = free_list.numel()
     _int32("free_list", free_list, (n_blocks,))
     _int32("free_count", free_count, (1,))
     if n_slots < 0:
         raise ValueError("n_slots: at least 0")
-    if free_count_out is None:
-        free_count_out = free_count
-    else:
+    count_in = count_out = free_count.data_ptr()
+    if free_count_out is not None:
         _int32("free_count_out", free_count_out, (1,))
+        count_out = free_count_out.data_ptr()
     # the outputs in one allocation
     if lens_out is None:
         slots, cu_new, lens_out, refused = lens.new_empty((n_slots + 2 * B + 2,)).split_with_sizes(
@@ -499,18 +515,12 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
         slots, cu_new, refused = lens.new_empty((n_slots + B + 2,)).split_with_sizes(
             (n_slots, B + 1, 1))
     st = lib().fq_page_step(lens.data_ptr(), new_lens.data_ptr(), B, block_tables.data_ptr(),
-                            max_blocks, page, free_list.data_ptr(), n_blocks,
-                            free_count.data_ptr(), lens_out.data_ptr(),
-                            free_count_out.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-                            n_slots, refused.data_ptr(), raw)
+                            max_blocks, page, free_list.data_ptr(), n_blocks, count_in,
+                            lens_out.data_ptr(), count_out, cu_new.data_ptr(), slots.data_ptr(),
+                            n_slots, refused.data_ptr(), tt.raw_stream(dev))
     if st:
         _check("fq_page_step", st)
     return lens_out, cu_new, slots, refused
-
-
-def _kv4_dtype(t) -> int:
-    import torch
-    return FQ_BF16 if t.dtype is torch.bfloat16 else _dtype_code(t)
 
 
 def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=None):
@@ -518,12 +528,14 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     them at slots [n] (int32; tokens with a slot outside the pool are skipped) of the cache
     [n_blocks, Hkv, page / 16, unit bytes].  With values=True returns the quantised values
     (k_values, v_values) [n, Hkv, d] in the inputs' type."""
-    dev = _device_index(k, v, slots, cache)
-    raw = _raw_stream(dev) if stream is None else None
-    if raw is None:
+    tt = _t()
+    dev = k.get_device()
+    if v.get_device() != dev or slots.get_device() != dev or cache.get_device() != dev:
+        raise ValueError("tensors on different devices")
+    if stream is not None or dev < 0 or tt.device() != dev:
         with _OnStream(dev, stream):
             return fq_kv4_write(k, v, slots, cache, group, values)
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype:
+    if k.shape != v.shape or k.dtype is not v.dtype:
         raise ValueError("k and v: two tensors [n, Hkv, d] of one type")
     n, hkv, d = k.shape
     k0, k1, k2 = k.stride()
@@ -534,12 +546,14 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     n_blocks, cache_hkv, page = _kv4_cache(cache, d, group)
     if cache_hkv != hkv:
         raise ValueError(f"cache of {cache_hkv} kv heads, keys of {hkv}")
+    kind = _kv4_type(k)
     kv = vv = kp = vp = None
     if values:
         kv, vv = k.new_empty((2, n, hkv, d)).unbind(0)
         kp, vp = kv.data_ptr(), vv.data_ptr()
-    st = lib().fq_kv4_write(k.data_ptr(), v.data_ptr(), _kv4_dtype(k), n, hkv, d, k0, k1, v0, v1,
-                            slots.data_ptr(), cache.data_ptr(), n_blocks, page, group, kp, vp, raw)
+    st = lib().fq_kv4_write(k.data_ptr(), v.data_ptr(), kind, n, hkv, d, k0, k1, v0, v1,
+                            slots.data_ptr(), cache.data_ptr(), n_blocks, page, group, kp, vp,
+                            tt.raw_stream(dev))
     if st:
         _check("fq_kv4_write", st)
     return (kv, vv) if values else None
@@ -553,44 +567,42 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: i
     (int32).  cu_q [B + 1] (int32) gives the sequences' rows of q, at most max_q each; without it
     every sequence has one.  window > 0: only the last `window` tokens are seen.  Returns out
     [n_q, Hq, d] of q's type."""
-    dev = _device_index(q, cache, block_tables, kv_lens, cu_q, out, workspace)
-    raw = _raw_stream(dev) if stream is None else None
-    if raw is None:
+    tt = _t()
+    dev = q.get_device()
+    _same_device(dev, cache, block_tables, kv_lens, cu_q, out, workspace)
+    if stream is not None or dev < 0 or tt.device() != dev:
         with _OnStream(dev, stream):
             return fq_kv4_attn(q, cache, block_tables, kv_lens, group, cu_q, max_q, window, scale,
                                out, workspace)
-    if q.dim() != 3 or block_tables.dim() != 2:
-        raise ValueError("q: [n_q, Hq, d]; block_tables: [B, max_blocks]")
     n_q, hq, d = q.shape
     q0, q1, q2 = q.stride()
     if n_q > 0 and q2 != 1:
         raise ValueError("q: the last axis has to be contiguous")
     n_blocks, hkv, page = _kv4_cache(cache, d, group)
-    B = kv_lens.numel()
-    max_blocks = block_tables.shape[1]
-    _int32("kv_lens", kv_lens, (B,))
+    B, max_blocks = block_tables.shape
     _int32("block_tables", block_tables, (B, max_blocks))
+    _int32("kv_lens", kv_lens, (B,))
     cu = None
     if cu_q is not None:
         _int32("cu_q", cu_q, (B + 1,))
         cu = cu_q.data_ptr()
+    kind = _kv4_type(q)
     if out is None:
         out = q.new_empty((n_q, hq, d))
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous():
         raise ValueError("out: a contiguous tensor of q's shape and type")
-    if workspace is None:
-        ws_bytes = _KV4_WS.get((hq, hkv, d, max_q))
-        if ws_bytes is None:
-            ws_bytes = fq_kv4_attn_workspace_bytes(hq, hkv, d, max_q)
-            _KV4_WS[hq, hkv, d, max_q] = ws_bytes
-        workspace = cache.new_empty((ws_bytes,))
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    st = lib().fq_kv4_attn(q.data_ptr(), _kv4_dtype(q), n_q, hq, d, q0, q1, cu, B, max_q,
-                           cache.data_ptr(), n_blocks, hkv, page, group, block_tables.data_ptr(),
-                           max_blocks, kv_lens.data_ptr(), window,
-                           1.0 / math.sqrt(d) if scale is None else scale, out.data_ptr(),
-                           workspace.data_ptr(), ws_bytes, raw)
+        ws_bytes = _kv4_size("fq_kv4_attn_workspace_bytes", B, hq, hkv, d, max_q, max_blocks, page)
+        if ws_bytes:
+            workspace = cache.new_empty((ws_bytes,))
+            ws = workspace.data_ptr()
+    st = lib().fq_kv4_attn(q.data_ptr(), kind, n_q, hq, d, q0, q1, cu, B, max_q, cache.data_ptr(),
+                           n_blocks, hkv, page, group, block_tables.data_ptr(), max_blocks,
+                           kv_lens.data_ptr(), window, d ** -0.5 if scale is None else scale,
+                           out.data_ptr(), ws, ws_bytes, tt.raw_stream(dev))
     if st:
         _check("fq_kv4_attn", st)
     return out

@@ -92,14 +92,16 @@ struct PageArgs {
 cudaError_t launch_write(const WriteArgs& a, cudaStream_t st);
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st);
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st);
-size_t attn_workspace_bytes(int d, int64_t rows);  // rows: query tokens x query heads of a kv head, at most
+size_t attn_workspace_bytes(int B, int hq, int hkv, int d, int max_q, int64_t capacity);
 cudaError_t launch_attn_rows(const AttnArgs& a, cudaStream_t st);  // many rows of a kv head
 size_t attn_rows_workspace_bytes(int d);
 cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_internal.h
 cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count);
 
-// Rows of a kv head up to which the register-fed kernel is the faster one.
-constexpr int64_t kFewRows = 16;
+// Rows of a kv head up to which the register-fed kernel is the faster one (24 sequences of 6,000 tokens, 4
+// kv heads, d = 128, 1 to n drafted tokens: 24 rows 52 us against 90, 64 rows 81 against 95, 96 rows 106
+// against 98; d = 64: 33 against 60, 49 against 61, 63 against 62).
+constexpr int64_t kFewRows = 64;
 
 }  // namespace kv4
 }  // namespace fq

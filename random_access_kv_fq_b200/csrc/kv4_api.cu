@@ -70,9 +70,12 @@ fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, i
   return from_cuda(launch_write(a, static_cast<cudaStream_t>(stream)));
 }
 
-size_t fq_kv4_attn_workspace_bytes(int Hq, int Hkv, int d, int max_q) {
-  if ((d != 64 && d != 128) || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_q < 0) return 0;
-  return attn_workspace_bytes(d, (int64_t)max_q * (Hq / Hkv));
+size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int max_blocks,
+                                   int page) {
+  if ((d != 64 && d != 128) || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_q < 1 ||
+      max_blocks < 0 || !page_ok(page))
+    return 0;
+  return attn_workspace_bytes(B, Hq, Hkv, d, max_q, (int64_t)max_blocks * page);
 }
 
 fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
@@ -95,7 +98,8 @@ fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
   if (!aligned(q, 2) || !aligned(out, 16) || !aligned(cu_q, 4) || !aligned(cache, 16) ||
       !aligned(block_tables, 4) || !aligned(kv_lens, 4))
     return FQ_ERR_ALIGNMENT;
-  if (!workspace || workspace_bytes < fq_kv4_attn_workspace_bytes(Hq, Hkv, d, max_q)) return FQ_ERR_WORKSPACE;
+  const size_t need = attn_workspace_bytes(B, Hq, Hkv, d, max_q, (int64_t)max_blocks * page);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FQ_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return FQ_ERR_ALIGNMENT;
   const AttnArgs a{q, type, n_q, Hq, d, q_token_stride, q_head_stride, cu_q, B, max_q, cache,
                    n_blocks, Hkv, page, group, block_tables, max_blocks, kv_lens, window, scale,

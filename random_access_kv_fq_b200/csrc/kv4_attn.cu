@@ -343,10 +343,10 @@ struct Warp {
           const uint32_t y = __byte_perm(w[2 * j][wi], w[2 * j + 1][wi], half ? 0x7632 : 0x5410);
           const uint32_t y8 = y >> 8;
           // 0x6400 + c is 1024 + c, 0x6400 + 16 c is 1024 + 16 c: back to c without rounding
-          const __half2 c0 = __hadd2(h2(and_or(y, 0x000F000Fu, 0x64006400u)), bias);
-          const __half2 c1 = __hfma2(h2(and_or(y, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
-          const __half2 c2 = __hadd2(h2(and_or(y8, 0x000F000Fu, 0x64006400u)), bias);
-          const __half2 c3 = __hfma2(h2(and_or(y8, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+          const __half2 c0 = __hadd2(h2(and_or<0x000F000Fu>(y, 0x64006400u)), bias);
+          const __half2 c1 = __hfma2(h2(and_or<0x00F000F0u>(y, 0x64006400u)), sixteenth, bias16);
+          const __half2 c2 = __hadd2(h2(and_or<0x000F000Fu>(y8, 0x64006400u)), bias);
+          const __half2 c3 = __hfma2(h2(and_or<0x00F000F0u>(y8, 0x64006400u)), sixteenth, bias16);
           v[j][0] = u32(__hfma2(c0, st[j], ze[j]));
           v[j][1] = u32(__hfma2(c1, st[j], ze[j]));
           v[j][2] = u32(__hfma2(c2, st[j], ze[j]));
@@ -760,6 +760,15 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
   }
 }
 
+// Row blocks of a sequence where every item gets a block of its own, or 0.  That is so where the items
+// fit the SMs at once and a warp's share is at most 8 units: no parts leave a block, and the second kernel
+// and the workspace fall away (one sequence of 517 tokens, 8 kv heads: 9.0 us against 11.9; with long
+// contexts ranges over all SMs win).
+int own_blocks(int B, int hkv, int max_q, int r, int64_t capacity, int nt, int warps) {
+  const int64_t blocks = ((int64_t)max_q * r + 8 * nt - 1) / (8 * nt);
+  return (int64_t)B * hkv * blocks <= kCtas && capacity <= 8 * kUnit * warps ? (int)blocks : 0;
+}
+
 template <typename T, int D, int G, int NT>
 cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   using P = Part<NT, D>;
@@ -779,15 +788,10 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   }
   int shift = 4;
   while ((1 << shift) < a.page) ++shift;
-  // A block to each item where they fit the SMs at once and a warp's share is at most 8 units: no
-  // parts leave a block, so the second kernel falls away (one sequence of 517 tokens, 8 kv heads:
-  // XXX us against YYY; at 4096 tokens the ranges over all SMs win).
-  const int r = a.hq / a.hkv, own = (int)(((int64_t)a.max_q * r + 8 * NT - 1) / (8 * NT));
-  const int64_t items = (int64_t)a.B * a.hkv * own;
-  const bool whole = items <= kCtas && (int64_t)a.max_blocks * a.page <= 8 * kUnit * W;
-  attn_kernel<T, D, G, NT><<<whole ? (unsigned)items : kCtas, 32 * W, bytes, st>>>(a, shift, whole ? own : 0);
+  const int r = a.hq / a.hkv, own = own_blocks(a.B, a.hkv, a.max_q, r, (int64_t)a.max_blocks * a.page, NT, W);
+  attn_kernel<T, D, G, NT><<<own ? (unsigned)(a.B * a.hkv * own) : kCtas, 32 * W, bytes, st>>>(a, shift, own);
   e = cudaGetLastError();
-  if (e != cudaSuccess || whole) return e;
+  if (e != cudaSuccess || own) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas);
   cfg.blockDim = dim3(256);
@@ -816,8 +820,11 @@ cudaError_t launch_shape(const AttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-size_t attn_workspace_bytes(int d, int64_t rows) {
+size_t attn_workspace_bytes(int B, int hq, int hkv, int d, int max_q, int64_t capacity) {
+  const int64_t rows = (int64_t)max_q * (hq / hkv);
   if (rows > kFewRows) return attn_rows_workspace_bytes(d);
+  const int nt = rows <= 8 ? 1 : 2, warps = nt == 1 ? kWarpsOf<1, 64> : d == 64 ? kWarpsOf<2, 64> : kWarpsOf<2, 128>;
+  if (own_blocks(B, hkv, max_q, hq / hkv, capacity, nt, warps)) return 0;
   return 2 * kCtas * (sizeof(PartHeader) + (d == 64 ? sizeof(Part<2, 64>) : sizeof(Part<2, 128>)));
 }
 

@@ -57,10 +57,11 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   return s;
 }
 
-// (x & mask) | bits in one instruction
-__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t bits) {
+// (x & MASK) | bits in one instruction, the mask in it
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t bits) {
   uint32_t y;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "r"(mask), "r"(bits));
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(y) : "r"(x), "n"(MASK), "r"(bits));
   return y;
 }
 

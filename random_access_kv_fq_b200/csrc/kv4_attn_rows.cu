@@ -84,12 +84,12 @@ __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity)
   return false;
 }
 // Warps that wait for an mbarrier are woken, and poll, whenever any mbarrier of the block moves: with all
-// 31 of them doing so half of the issued instructions were polls.  So one warp of a group waits, and the
-// others for it at a named barrier.
+// 31 of them doing so half of the issued instructions were polls.  So one softmax warp waits for the
+// scores, and the others for it at a named barrier.
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-enum { kBarSoftmax = 1, kBarPair = 2, kBarKeys = 6, kBarValues = 7 };
+enum { kBarSoftmax = 1, kBarPair = 2 };
 
 // The items of a block's range of the line, one at a time, the same in every role.
 template <int D>
@@ -143,10 +143,10 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint3
 __device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) {
   const __half2 bias = h2(0xE400E400u), sixteenth = h2(0x2C002C00u), bias16 = h2(0xD400D400u);
   const uint32_t w8 = w >> 8;
-  c[0] = __hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), bias);
-  c[1] = __hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
-  c[2] = __hadd2(h2(and_or(w8, 0x000F000Fu, 0x64006400u)), bias);
-  c[3] = __hfma2(h2(and_or(w8, 0x00F000F0u, 0x64006400u)), sixteenth, bias16);
+  c[0] = __hadd2(h2(and_or<0x000F000Fu>(w, 0x64006400u)), bias);
+  c[1] = __hfma2(h2(and_or<0x00F000F0u>(w, 0x64006400u)), sixteenth, bias16);
+  c[2] = __hadd2(h2(and_or<0x000F000Fu>(w8, 0x64006400u)), bias);
+  c[3] = __hfma2(h2(and_or<0x00F000F0u>(w8, 0x64006400u)), sixteenth, bias16);
 }
 
 // Eight tokens' keys (16 for d = 64), from row `row` of a tile on: 32 lanes, each a 16-byte chunk (4
@@ -547,17 +547,16 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     constexpr int kStep = 1024 / D;  // tokens of a warp's step
     const bool keys = warp < kSoftmaxWarps + kKeyWarps;
     const int ch = lane % (D / 32), row_lane = lane / (D / 32);
-    const bool leads = (warp & 3) == 0;
     uint32_t chunk = 0;
     for (bool begun = false; it.next(a, r, begun); begun = true) {
       for (int j = it.t0; j < it.t1; ++j, ++tile) {
         const uint32_t buf = tile & 1, base = smem32 + buf * C::kBuf;
         // keys are done with when their scores are, values when the products with the weights are
-        if (leads && tile >= 2) wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1);
+        if (tile >= 2) wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1);
         for (int c = 0; c < C::kChunks; ++c, ++chunk) {
           const uint32_t slot = chunk % kRing;
-          if (leads) wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
-          named_sync(keys ? kBarKeys : kBarValues, 128);
+          wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
+          __syncwarp();
           const uint32_t at = packed32 + ((keys ? 0 : kRing) + slot) * C::kPacked;
           const int row0 = c * C::kChunkUnits * kUnit, in_chunk = (warp & 3) * kStep + row_lane, row = row0 + in_chunk;  // of the tile
           const uint32_t codes_at = at + in_chunk / kUnit * (kUnit * D / 2), scales_at = at + C::kCodes + in_chunk / kUnit * (64 * C::NG);

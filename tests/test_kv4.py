@@ -71,7 +71,7 @@ def _write_args(**kw):
 
 def _attn_args(**kw):
     a = dict(q=BASE, type=0, n_q=3, hq=8, d=64, qt=512, qh=64, cu=None, B=3, max_q=1, cache=BASE, n_blocks=8, hkv=2,
-             page=16, group=32, tables=BASE, mb=4, lens=BASE, window=0, scale=ctypes.c_float(0.1), out=BASE, ws=BASE,
+             page=16, group=32, tables=BASE, mb=4096, lens=BASE, window=0, scale=ctypes.c_float(0.1), out=BASE, ws=BASE,
              ws_bytes=1 << 30, stream=None)
     a.update(kw)
     return list(a.values())
@@ -121,8 +121,11 @@ def test_page_step_refuses(edit, status):
 def test_sizes():
     assert fq.fq_kv4_unit_bytes(96, 32) == 0 and fq.fq_kv4_unit_bytes(64, 128) == 0 and fq.fq_kv4_unit_bytes(128, 0) == 0
     ws = fq.fq_kv4_attn_workspace_bytes
-    assert ws(8, 1, 64, 1) > 0 and ws(32, 8, 128, 1) > 0 and ws(32, 8, 128, 64) > ws(32, 8, 128, 1)
-    assert ws(8, 1, 80, 1) == 0 and ws(7, 2, 64, 1) == 0 and ws(8, 0, 64, 1) == 0 and ws(8, 1, 64, -1) == 0
+    assert ws(64, 8, 1, 64, 1, 2048, 16) > 0 and ws(1, 32, 8, 128, 1, 2048, 16) > 0
+    assert ws(8, 32, 8, 128, 64, 16, 16) > ws(64, 32, 8, 128, 1, 16, 16) > 0
+    assert ws(1, 32, 8, 128, 1, 16, 16) == 0  # nothing is split
+    for bad in ((4, 8, 1, 80, 1, 4, 16), (4, 7, 2, 64, 1, 4, 16), (4, 8, 0, 64, 1, 4, 16), (4, 8, 1, 64, -1, 4, 16), (4, 8, 1, 64, 1, 4, 20)):
+        assert ws(*bad) == 0
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():
