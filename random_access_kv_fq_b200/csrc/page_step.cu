@@ -8,8 +8,8 @@
 // sums, pages, slots).  One launch: every block of one cluster computes the sums itself (B values
 // from L2, the sums in shared memory), so no block waits for another's sums; two cluster barriers
 // order (1) all reads of lens and free_count before they may be overwritten in place and (2)
-// released pages before they are handed out again.  A warp writes 256 slots at a time: it finds the
-// requests of the first and the last by bisection and its lanes search only between them.
+// released pages before they are handed out again.  A warp writes 32 or 256 slots at a time: it finds
+// the requests of the first and the last by bisection and its lanes search only between them.
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -23,7 +23,6 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;
-constexpr int kSlots = 8;  // slots of a lane at a time: their table reads are in flight together
 
 __device__ __forceinline__ int sat(int64_t x) { return x > INT_MAX ? INT_MAX : (int)x; }
 
@@ -64,10 +63,24 @@ __device__ __forceinline__ int last_le(const int* a, int lo, int hi, int x) {
   return lo;
 }
 
+// The same by a whole warp, 32 places at a time.
+__device__ __forceinline__ int warp_last_le(const int* a, int lo, int hi, int x) {
+  const int lane = threadIdx.x & 31;
+  while (hi - lo > 1) {
+    const int stride = (hi - lo + 31) / 32, i = lo + lane * stride;
+    lo += (__popc(__ballot_sync(~0u, i < hi && a[i] <= x)) - 1) * stride;
+    hi = min(hi, lo + stride);
+  }
+  return lo;
+}
+
 template <bool ALONE>
 __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_shift) {
+  // slots of a lane at a time: in a large step their searches and table reads are in flight together
+  constexpr int kSlots = ALONE ? 1 : 8;
   extern __shared__ int sums[];
   __shared__ Two part[32];
+  __shared__ int taken, refused;
   int* cu = sums;              // [B + 1] first new token of a request
   int* off = cu + a.B + 1;     // [B]     first new page
   int* rel = off + a.B;        // [B]     first released page
@@ -84,6 +97,7 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
   const int count = min(max(__ldcg(a.free_count), 0), a.n_blocks);
   const auto pages_of = [&](int64_t tokens) { return (tokens + a.page - 1) >> page_shift; };
 
+  if (threadIdx.x == 0) taken = refused = 0;
   // this thread's requests: tokens to add and pages to release
   Two mine{0, 0}, total;
   for (int b = b0; b < b1; ++b) {
@@ -113,7 +127,7 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
   }
   int64_t upto = block_scan(need, part, total).a;
   // a request that fits is served while the pages needed up to it are there
-  Two done{0, 0};  // pages handed out, requests refused
+  int last_page = 0, turned_away = 0;  // behind the last page handed out; requests refused
   at = first.a;
   for (int b = b0; b < b1; ++b) {
     const int add = off[b];
@@ -126,13 +140,17 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
     upto += n;
     if (!fits || (n > 0 && upto > avail)) {
       held[b] = ~held[b];
-      ++done.b;
-    } else {
-      done.a += n;
+      ++turned_away;
+    } else if (n > 0) {
+      last_page = (int)upto;
     }
   }
-  block_scan(done, part, total);
-  const int taken = (int)total.a;
+  last_page = __reduce_max_sync(~0u, last_page);
+  turned_away = __reduce_add_sync(~0u, turned_away);
+  if ((threadIdx.x & 31) == 0) {
+    atomicMax(&taken, last_page);
+    atomicAdd(&refused, turned_away);
+  }
   if (threadIdx.x == 0) cu[a.B] = sat(total_tokens);
   all_blocks();  // the sums are there; lens and free_count are read and may be overwritten
 
@@ -144,7 +162,7 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
   for (int b = me; b <= a.B; b += n_thr) a.cu_new[b] = cu[b];
   if (me == 0) {
     *a.free_count_out = avail - taken;
-    *a.refused = (int)total.b;
+    *a.refused = refused;
   }
   if (avail > count) {
     for (int r = me; r < avail - count; r += n_thr) {
@@ -162,17 +180,40 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
   for (int i0 = (me >> 5) * 32 * kSlots; i0 < a.n_slots; i0 += n_thr * kSlots) {
     int lo = 0, hi = 1;
     if (i0 < written) {
-      lo = last_le(cu, 0, a.B, i0);
-      hi = last_le(cu, lo, a.B, min(i0 + 32 * kSlots, written) - 1) + 1;
+      lo = warp_last_le(cu, 0, a.B, i0);
+      const int last = min(i0 + 32 * kSlots, written) - 1;
+      hi = cu[lo + 1] > last ? lo + 1 : warp_last_le(cu, lo, a.B, last) + 1;
     }
-    int id[kSlots], in[kSlots];
+    if (!ALONE && hi - lo == 1 && i0 + 32 * kSlots <= written) {
+      // all 256 of one request
+      const int h = held[lo], pages = (int)pages_of(h), first_pos = h + (i0 + lane - cu[lo]);
+      const int32_t* row = a.tables + (int64_t)lo * a.max_blocks;
+      const int32_t* fresh = a.free_list + (avail - 1 - off[lo] + pages);  // page pg >= pages is fresh[-pg]
+      int id[kSlots];
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k) {
+        const int pg = (first_pos + 32 * k) >> page_shift;
+        id[k] = h < 0 ? -1 : pg < pages ? row[pg] : __ldcg(fresh - pg);
+      }
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k)
+        a.slots[i0 + 32 * k + lane] = (unsigned)id[k] < (unsigned)a.n_blocks ? (id[k] << page_shift) + ((first_pos + 32 * k) & (a.page - 1)) : -1;
+      continue;
+    }
+    int at[kSlots], id[kSlots], in[kSlots];
+#pragma unroll
+    for (int k = 0; k < kSlots; ++k) at[k] = lo;
+    for (int step = hi - lo > 1 ? 1 << (31 - __clz(hi - lo)) : 0; step; step >>= 1) {
+#pragma unroll
+      for (int k = 0; k < kSlots; ++k)
+        if (at[k] + step < hi && cu[at[k] + step] <= i0 + 32 * k + lane) at[k] += step;
+    }
 #pragma unroll
     for (int k = 0; k < kSlots; ++k) {
-      const int i = i0 + 32 * k + lane;
+      const int i = i0 + 32 * k + lane, b = at[k];
       id[k] = -1;
       in[k] = 0;
       if (i < written) {
-        const int b = last_le(cu, lo, hi, i);
         const int h = held[b];
         if (h >= 0) {
           const int pos = h + (i - cu[b]), pg = pos >> page_shift, pages = (int)pages_of(h);
