@@ -430,21 +430,23 @@ __device__ __forceinline__ void write_merged(const AttnArgs& a, const PartHeader
   }
 }
 
-// Running join of an item's parts, for one fragment word: rows 0 and 1 of its four numbers.
+// Join of an item's parts, for one fragment word: rows 0 and 1 of its four numbers.  The maxima are known
+// before, so that the parts' numbers wait only for their own weights.
 struct Join {
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
+  __device__ __forceinline__ void top(float2 m) {
+    m0 = fmaxf(m0, m.x);
+    m1 = fmaxf(m1, m.y);
+  }
   __device__ __forceinline__ void add(float4 y, float2 m, float2 l) {
-    const float n0 = fmaxf(m0, m.x), n1 = fmaxf(m1, m.y);
-    const float a0 = ex2(m0 - n0), a1 = ex2(m1 - n1), b0 = ex2(m.x - n0), b1 = ex2(m.y - n1);
-    o.x = fmaf(y.x, b0, o.x * a0);
-    o.y = fmaf(y.y, b1, o.y * a1);
-    o.z = fmaf(y.z, b0, o.z * a0);
-    o.w = fmaf(y.w, b1, o.w * a1);
-    l0 = fmaf(l.x, b0, l0 * a0);
-    l1 = fmaf(l.y, b1, l1 * a1);
-    m0 = n0;
-    m1 = n1;
+    const float b0 = ex2(m.x - m0), b1 = ex2(m.y - m1);
+    o.x = fmaf(y.x, b0, o.x);
+    o.y = fmaf(y.y, b1, o.y);
+    o.z = fmaf(y.z, b0, o.z);
+    o.w = fmaf(y.w, b1, o.w);
+    l0 = fmaf(l.x, b0, l0);
+    l1 = fmaf(l.y, b1, l1);
   }
 };
 
@@ -459,8 +461,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
   P* heads = reinterpret_cast<P*>(smem + W * kSlot);              // [W]
   __shared__ uint64_t bars[W][kStages];
   __shared__ PartHeader hdr[W][2];
-  __shared__ int64_t scan[W], start_in[W];
-  __shared__ int start_b[W];
+  __shared__ int64_t scan[W];
   __shared__ int4 groups[2 * W];
   __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -494,15 +495,15 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       left = warp == 0 ? kItemUnits + 1 : 1;
     }
   } else {
-    // The line of all items' costs: each thread adds up its sequences', and the one whose cost
-    // holds the start of a warp's range tells that warp.
+    // The line of all items' costs: running sums over groups of `per` sequences, in shared memory where
+    // the rings will be, in which each warp looks up its range's start.
     const int per = (a.B + 32 * W - 1) / (32 * W), b0 = tid * per, b1 = min(a.B, b0 + per);
-    int64_t mine = 0;
+    int64_t* sums = reinterpret_cast<int64_t*>(smem);
+    int64_t x = 0;
     for (int i = b0; i < b1; ++i) {
       s = load_seq<NB, kUnit, kItemUnits>(a, i, r);
-      mine += (int64_t)(a.hkv * s.blocks) * s.cost;
+      x += (int64_t)(a.hkv * s.blocks) * s.cost;
     }
-    int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const int64_t y = __shfl_up_sync(~0u, x, d);
@@ -510,45 +511,44 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     }
     if (lane == 31) scan[warp] = x;
     __syncthreads();
-    int64_t below = x - mine, total = 0;
-#pragma unroll 1
-    for (int w = 0; w < W; ++w) {
-      if (w < warp) below += scan[w];
-      total += scan[w];
+    // the sums of the warps, by every warp
+    int64_t all = lane < W ? scan[lane] : 0;
+#pragma unroll
+    for (int d = 1; d < W; d <<= 1) {
+      const int64_t y = __shfl_up_sync(~0u, all, d);
+      if (lane >= d) all += y;
     }
-    const int64_t span = max((int64_t)(total * (1.0 / (kCtas * W))) + 1, (int64_t)kChunk);
-    const int64_t block0 = (int64_t)blockIdx.x * W * span;
-    if (below + mine > block0 && below < block0 + W * span) {
-      for (int i = b0; i < b1; ++i) {
-        if (per > 1) {
-          s = load_seq<NB, kUnit, kItemUnits>(a, i, r);
-          mine = (int64_t)(a.hkv * s.blocks) * s.cost;
-        }
-#pragma unroll 1
-        for (int w = 0; w < W; ++w) {
-          const int64_t x0 = block0 + w * span - below;
-          if (x0 >= 0 && x0 < mine) {
-            start_b[w] = i;
-            start_in[w] = x0;
-          }
-        }
-        below += mine;
-      }
-    }
+    const int64_t total = __shfl_sync(~0u, all, W - 1), before = __shfl_sync(~0u, all, warp > 0 ? warp - 1 : 0);
+    sums[tid] = x + (warp > 0 ? before : 0);
+    ptx::fence_proxy_async_smem();  // copies will write where the sums are
     __syncthreads();
-    left = min(span, total - block0 - warp * span);
+    const int64_t span = max((int64_t)(total * (1.0 / (kCtas * W))) + 1, (int64_t)kChunk);
+    const int64_t x0 = (int64_t)(blockIdx.x * W + warp) * span;
+    left = min(span, total - x0);
     if (left > 0) {
-      b = start_b[warp];
-      s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
-      const int64_t in_seq = start_in[warp];
+      // the first group whose sum is past x0, 32 places at a time
+      int lo = 0, n = 32 * W;
+      while (n > 1) {
+        const int step = (n + 31) / 32, i = min(lo + (lane + 1) * step, lo + n) - 1;
+        lo += (__ffs(__ballot_sync(~0u, sums[i] > x0)) - 1) * step;
+        n = step;
+      }
+      int64_t in_seq = x0 - (lo > 0 ? sums[lo - 1] : 0);
+      for (b = lo * per;; ++b) {
+        s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
+        const int64_t cost = (int64_t)(a.hkv * s.blocks) * s.cost;
+        if (in_seq < cost) break;
+        in_seq -= cost;
+      }
       // which of the sequence's items, all of one cost; the estimate is off by one at most
-      int64_t item = (int64_t)((double)in_seq / s.cost);
-      if (item * s.cost > in_seq) --item;
-      if (in_seq - item * s.cost >= s.cost) ++item;
-      from = (int)(in_seq - item * s.cost);
-      head = (int)item / s.blocks;
-      block = (int)item - head * s.blocks;
+      int item = (int)((float)in_seq / (float)s.cost);
+      if ((int64_t)item * s.cost > in_seq) --item;
+      if (in_seq - (int64_t)item * s.cost >= s.cost) ++item;
+      from = (int)(in_seq - (int64_t)item * s.cost);
+      head = s.blocks == 1 ? item : item / s.blocks;
+      block = item - head * s.blocks;
     }
+    __syncthreads();  // the sums are read
   }
   while (left > 0 && ok) {
     const int to = (int)min((int64_t)s.cost, from + left);
@@ -705,9 +705,15 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     const int4 gr = groups[i / E];
     const int e = i % E, row = ((e >> 5) / W_::MT) * 8 + 2 * (e & 3);
     Join join;
-    for (int c = 0; c < gr.y; ++c) {
-      const int w = (gr.x >> 1) + c;
-      const P& p = c == 0 && (gr.x & 1) ? *reinterpret_cast<const P*>(rings + w * kSlot) : heads[w];
+    const int w0 = gr.x >> 1;
+    const P& first = gr.x & 1 ? *reinterpret_cast<const P*>(rings + w0 * kSlot) : heads[w0];
+    join.top(*reinterpret_cast<const float2*>(&first.m[row]));
+#pragma unroll 4
+    for (int c = 1; c < gr.y; ++c) join.top(*reinterpret_cast<const float2*>(&heads[w0 + c].m[row]));
+    join.add(first.o[e], *reinterpret_cast<const float2*>(&first.m[row]), *reinterpret_cast<const float2*>(&first.l[row]));
+#pragma unroll 4
+    for (int c = 1; c < gr.y; ++c) {
+      const P& p = heads[w0 + c];
       join.add(p.o[e], *reinterpret_cast<const float2*>(&p.m[row]), *reinterpret_cast<const float2*>(&p.l[row]));
     }
     if ((gr.x & 1) && gr.z) {
@@ -738,23 +744,12 @@ __global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
   for (int e = threadIdx.x; e < NT * D / 16 * 32; e += blockDim.x) {
     const int row = ((e >> 5) / (D / 16)) * 8 + 2 * (e & 3);
     Join join;
-    for (int c = c0; c <= end; c += 8) {
-      float4 o[8];
-      float2 m[8], l[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m[i] = make_float2(-FLT_MAX, -FLT_MAX);
-        l[i] = make_float2(0.f, 0.f);
-        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c + i <= end) {
-          const P& p = part[(c + i) * 2 + (c + i == c0)];
-          o[i] = p.o[e];
-          m[i] = *reinterpret_cast<const float2*>(&p.m[row]);
-          l[i] = *reinterpret_cast<const float2*>(&p.l[row]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) join.add(o[i], m[i], l[i]);
+#pragma unroll 8
+    for (int c = c0; c <= end; ++c) join.top(*reinterpret_cast<const float2*>(&part[c * 2 + (c == c0)].m[row]));
+#pragma unroll 8
+    for (int c = c0; c <= end; ++c) {
+      const P& p = part[c * 2 + (c == c0)];
+      join.add(p.o[e], *reinterpret_cast<const float2*>(&p.m[row]), *reinterpret_cast<const float2*>(&p.l[row]));
     }
     write_merged<T, D, NT>(a, h, e, join.o, join.l0, join.l1);
   }
