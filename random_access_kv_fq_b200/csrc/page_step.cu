@@ -235,9 +235,11 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
 
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(int) * (4 * (size_t)a.B + 1);
-  // One block does a small step (256 decodes: XXX us, with the cluster YYY); a cluster shares the
-  // stores of a large one.  Few requests need few warps: their sums are sooner there.
-  const bool alone = (int64_t)a.n_slots + a.B <= 8192;
+  // One block does a small step: its barriers cost less.  A cluster shares the searches and stores of a
+  // large one.  In us, one block and the cluster: 256 decodes 5.0 and 6.8, with every 17th request
+  // released 8.6 and 8.0; 1,024 such requests 14.1 and 11.1; 4,096 of them 36.2 and 16.7.
+  // Few requests need few warps: their sums are sooner there.
+  const bool alone = (int64_t)a.n_slots + a.B <= 1024;
   const auto kernel = alone ? page_step_kernel<true> : page_step_kernel<false>;
   if (smem > 48 * 1024 - sizeof(Two) * 32) {  // what a block may have unasked
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
