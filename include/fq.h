@@ -417,8 +417,8 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
  *             sequence has are left as they were.
  *   workspace fq_kv4_attn_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0), owned by the
- *             caller and overwritten; calls that may overlap (two streams, two captured graphs) need
- *             one each.
+ *             caller, of any content, and overwritten; calls that may overlap (two streams, two captured
+ *             graphs) need one each.
  * Precondition: the groups of tokens that are seen span less than 65504 (15 s and c s + z are fp16
  * numbers on the way).
  * B <= 8192, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.

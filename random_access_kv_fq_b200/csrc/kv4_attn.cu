@@ -15,7 +15,8 @@
 //   softmax  base 2, against a running maximum that moves only when a score passes it by 8.
 //   values   O^T += V^T P^T with V = fp16(c s + z) and P in fp16, for fp16 outputs in two parts:
 //            one rounding of 2^-12 then, beside the output's own; bf16's own is 2^-9.
-// A warp's unfinished ranges are joined in shared memory, a block's in a second small kernel.
+// A warp's unfinished ranges are joined in shared memory, a block's by the last block to leave a part
+// of the item.
 //
 // mma.sync and not tcgen05: the products of decode are 8 to 16 rows wide, operands come out of
 // registers, and the tensor pipe has three quarters of its time left at the HBM bound.
@@ -46,6 +47,21 @@ struct Part {
   float4 o[NT * D / 16 * 32];  // accumulators in fragment order
   float m[8 * NT], l[8 * NT];
 };
+
+// What a warp says of a part that it leaves.
+struct PartHeader {
+  int state;               // 0: none, 1: the item goes on, 3: its last part
+  int q0, rows, head, rb;  // where its rows are
+  int cost;                // of the whole item,
+  int64_t start;           // and where it begins on the line
+};
+
+// Blocks that have left a part of the item begun in block c, at the workspace's start: the call's tag
+// and the number.  The workspace needs no preparation: a word without the call's tag counts as none.
+// The last block leaves the tag with 0, for a replay of the same call.
+constexpr int kCountBits = 8;
+static_assert(kCtas < 1 << kCountBits, "");
+constexpr size_t kCounters = (kCtas * sizeof(uint64_t) + 15) / 16 * 16;
 
 // ------------------------------------------------------------------------------ items
 
@@ -414,44 +430,113 @@ struct Warp {
   }
 };
 
-// One fragment word of an item's merged accumulators into out: rows 2 t and 2 t + 1, two coordinates.
-template <typename T, int D, int NT>
-__device__ __forceinline__ void write_merged(const AttnArgs& a, const PartHeader& h, int e, float4 o, float l0, float l1) {
-  const int lane = e & 31, mt = (e >> 5) % (D / 16), nt = (e >> 5) / (D / 16), g = lane >> 2, t = lane & 3;
-  const uint32_t r = a.hq / a.hkv;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    const uint32_t row = h.rb * 8 * NT + nt * 8 + 2 * t + c;
-    if (row >= (uint32_t)h.rows) continue;
-    const uint32_t tok = row / r;
-    const float l = c ? l1 : l0, inv = l > 0.f ? 1.0f / l : 0.f;
-    T* dst = static_cast<T*>(a.out) + ((int64_t)(h.q0 + tok) * a.hq + h.head * r + row - tok * r) * D + g * (D / 8) + 2 * mt;
-    *reinterpret_cast<uint32_t*>(dst) = pack_out<T>((c ? o.y : o.x) * inv, (c ? o.w : o.z) * inv);
-  }
-}
+// N fragment words of an item's rows nt * 8 + 2 t and + 1: two coordinates each, all of one row adjacent.
+// A warp's piece of a join.
+template <int NT, int D>
+struct Words {
+  static constexpr int N = D / 32, kPieces = NT * D / 16 / N;
+  float4 o[N];
+  float2 l;
 
-// Join of an item's parts, for one fragment word: rows 0 and 1 of its four numbers.  The maxima are known
-// before, so that the parts' numbers wait only for their own weights.
-struct Join {
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  float m0 = -FLT_MAX, m1 = -FLT_MAX, l0 = 0.f, l1 = 0.f;
-  __device__ __forceinline__ void top(float2 m) {
-    m0 = fmaxf(m0, m.x);
-    m1 = fmaxf(m1, m.y);
+  static __device__ __forceinline__ int row(int piece, int lane) { return piece * N / (D / 16) * 8 + 2 * (lane & 3); }
+
+  // Sums the parts at(0) .. at(n - 1) of this block.  The maxima come first, so that the numbers wait
+  // only for their own weights.
+  template <typename At>
+  __device__ __forceinline__ float2 join(int piece, int lane, int n, const At& at) {
+    const int r0 = row(piece, lane);
+    float2 top = make_float2(-FLT_MAX, -FLT_MAX);
+#pragma unroll 4
+    for (int c = 0; c < n; ++c) {
+      const float2 m = *reinterpret_cast<const float2*>(&at(c)->m[r0]);
+      top.x = fmaxf(top.x, m.x);
+      top.y = fmaxf(top.y, m.y);
+    }
+    clear();
+#pragma unroll 2
+    for (int c = 0; c < n; ++c) {
+      const Part<NT, D>* p = at(c);
+      const float2 m = *reinterpret_cast<const float2*>(&p->m[r0]);
+      add(p->o + piece * N * 32 + lane, *reinterpret_cast<const float2*>(&p->l[r0]), ex2(m.x - top.x), ex2(m.y - top.y));
+    }
+    return top;
   }
-  __device__ __forceinline__ void add(float4 y, float2 m, float2 l) {
-    const float b0 = ex2(m.x - m0), b1 = ex2(m.y - m1);
-    o.x = fmaf(y.x, b0, o.x);
-    o.y = fmaf(y.y, b1, o.y);
-    o.z = fmaf(y.z, b0, o.z);
-    o.w = fmaf(y.w, b1, o.w);
-    l0 = fmaf(l.x, b0, l0);
-    l1 = fmaf(l.y, b1, l1);
+
+  // The same for parts of other blocks: everything of a part is asked for at once, against a running
+  // maximum.
+  template <typename At>
+  __device__ __forceinline__ float2 join_far(int piece, int lane, int n, const At& at) {
+    const int r0 = row(piece, lane);
+    float2 top = make_float2(-FLT_MAX, -FLT_MAX);
+    clear();
+#pragma unroll 2
+    for (int c = 0; c < n; ++c) {
+      const Part<NT, D>* p = at(c);
+      const float2 m = __ldcg(reinterpret_cast<const float2*>(&p->m[r0])), s = __ldcg(reinterpret_cast<const float2*>(&p->l[r0]));
+      float4 y[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) y[i] = __ldcg(p->o + (piece * N + i) * 32 + lane);
+      const float2 up = make_float2(fmaxf(top.x, m.x), fmaxf(top.y, m.y));
+      const float f0 = ex2(top.x - up.x), f1 = ex2(top.y - up.y);
+      l.x *= f0;
+      l.y *= f1;
+#pragma unroll
+      for (int i = 0; i < N; ++i) o[i] = make_float4(o[i].x * f0, o[i].y * f1, o[i].z * f0, o[i].w * f1);
+      top = up;
+      add<1>(y, s, ex2(m.x - up.x), ex2(m.y - up.y));
+    }
+    return top;
+  }
+
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+    l = make_float2(0.f, 0.f);
+  }
+
+  template <int STEP = 32>
+  __device__ __forceinline__ void add(const float4* y, float2 s, float w0, float w1) {
+    l.x = fmaf(s.x, w0, l.x);
+    l.y = fmaf(s.y, w1, l.y);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float4 v = y[i * STEP];
+      o[i] = make_float4(fmaf(v.x, w0, o[i].x), fmaf(v.y, w1, o[i].y), fmaf(v.z, w0, o[i].z), fmaf(v.w, w1, o[i].w));
+    }
+  }
+
+  __device__ __forceinline__ void leave(Part<NT, D>* dst, int piece, int lane, float2 top) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) dst->o[(piece * N + i) * 32 + lane] = o[i];
+    if (piece * N % (D / 16) == 0 && lane < 4) {
+      const int r0 = row(piece, lane);
+      *reinterpret_cast<float2*>(&dst->m[r0]) = top;
+      *reinterpret_cast<float2*>(&dst->l[r0]) = l;
+    }
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void write(const AttnArgs& a, const PartHeader& h, int piece, int lane) const {
+    const uint32_t r = a.hq / a.hkv;
+    const int word = piece * N % (D / 16);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t at = h.rb * 8 * NT + row(piece, lane) + c;
+      if (at >= (uint32_t)h.rows) continue;
+      const uint32_t tok = at / r;
+      const float sum = c ? l.y : l.x, inv = sum > 0.f ? 1.0f / sum : 0.f;
+      T* dst = static_cast<T*>(a.out) + ((int64_t)(h.q0 + tok) * a.hq + h.head * r + at - tok * r) * D + (lane >> 2) * (D / 8) + 2 * word;
+      uint32_t v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = pack_out<T>((c ? o[i].y : o[i].x) * inv, (c ? o[i].w : o[i].z) * inv);
+      if constexpr (N == 4) *reinterpret_cast<uint4*>(dst) = make_uint4(v[0], v[1], v[2], v[3]);
+      else *reinterpret_cast<uint2*>(dst) = make_uint2(v[0], v[1]);
+    }
   }
 };
 
 template <typename T, int D, int G, int NT>
-__global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs a, int page_shift, int own_blocks) {
+__global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs a, int page_shift, int own_blocks, uint64_t tag) {
   using W_ = Warp<T, D, G, NT>;
   using P = Part<NT, D>;
   constexpr int W = kWarpsOf<NT, D>, NB = 8 * NT, UB = W_::UB, kStages = kStagesOf<D>;
@@ -462,7 +547,9 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
   __shared__ uint64_t bars[W][kStages];
   __shared__ PartHeader hdr[W][2];
   __shared__ int64_t scan[W];
-  __shared__ int4 groups[2 * W];
+  __shared__ int64_t range_end[W];
+  __shared__ int4 closing[2];
+  __shared__ uint32_t groups[2 * W];  // an item's first slot, its parts << 8, whether others join it << 16
   __shared__ int gave_up;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = a.hq / a.hkv;
@@ -480,7 +567,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
   bool ok = true;
   // What is left of this warp's range of the line, where it begins in its first item, and that item:
   // number `block` of the row blocks of (sequence b, kv head).
-  int64_t left = 0;
+  int64_t left = 0, span = 1;
   int from = 0, b = 0, head = 0, block = 0;
   Seq s = {};
   if (own_blocks > 0) {
@@ -522,9 +609,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     sums[tid] = x + (warp > 0 ? before : 0);
     ptx::fence_proxy_async_smem();  // copies will write where the sums are
     __syncthreads();
-    const int64_t span = max((int64_t)(total * (1.0 / (kCtas * W))) + 1, (int64_t)kChunk);
+    span = max((int64_t)(total * (1.0 / (kCtas * W))) + 1, (int64_t)kChunk);
     const int64_t x0 = (int64_t)(blockIdx.x * W + warp) * span;
     left = min(span, total - x0);
+    range_end[warp] = x0 + left;
     if (left > 0) {
       // the first group whose sum is past x0, 32 places at a time
       int lo = 0, n = 32 * W;
@@ -550,7 +638,8 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     }
     __syncthreads();  // the sums are read
   }
-  while (left > 0 && ok) {
+  // after a wait that gave up the rest of the range counts as empty, so that each item gets its parts
+  while (left > 0) {
     const int to = (int)min((int64_t)s.cost, from + left);
     left -= to - from;
     // Row blocks from both ends in turn: later ones see more tokens, two neighbours about as many as
@@ -572,7 +661,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     const int u0 = share(from), u1 = share(to);
 
     st.reset();
-    if (u0 < u1) {
+    if (u0 < u1 && ok) {
       // Copies run up to kStages chunks ahead.  Lane i issues units i, i + 32, ... of the range, from
       // the table entry that it holds; a unit behind the range or on a page outside the pool only
       // counts as arrived, and `gone` has its bit.
@@ -656,7 +745,10 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       // an item begun before this range leaves its part beside the ring, one that goes on in it
       const int k = from > 0 ? 0 : 1;
       st.write_part(k == 0 ? heads + warp : reinterpret_cast<P*>(ring), lane);
-      if (lane == 0) hdr[warp][k] = PartHeader{to == s.cost ? 3 : 1, s.q0, s.rows, head, rb};
+      if (lane == 0) {
+        const int64_t start = own_blocks > 0 ? 0 : range_end[warp] - left - to;
+        hdr[warp][k] = PartHeader{to == s.cost ? 3 : 1, s.q0, s.rows, head, rb, s.cost, start};
+      }
     }
     // the next item of the line
     from = 0;
@@ -669,19 +761,21 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     }
   }
   if (!ok) gave_up = 1;
-  asm volatile("griddepcontrol.launch_dependents;");
   __syncthreads();
   if (tid == 0 && gave_up) atomicAdd(&g_kv4_wait_timeouts, 1u);
 
   // Join the parts of each item; what begins before or ends behind the block goes to the workspace.
   // Slot 2 w + k holds part k of warp w.  An item's parts are a part 1 (or, if begun before the
   // block, warp 0's part 0) and the next warps' parts 0 up to its last one.
-  PartHeader* out_hdr = static_cast<PartHeader*>(a.workspace);
-  P* out_part = reinterpret_cast<P*>(static_cast<uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
+  uint64_t* counters = static_cast<uint64_t*>(a.workspace);
+  P* out_part = reinterpret_cast<P*>(static_cast<uint8_t*>(a.workspace) + kCounters);  // [kCtas][2]
   const int state = lane < 2 * W ? hdr[lane >> 1][lane & 1].state : 0;
   const uint32_t has = __ballot_sync(~0u, state != 0), ends = __ballot_sync(~0u, state == 3) & 0x55555555u;
   const bool begins = state != 0 && ((lane & 1) || lane == 0);
   const uint32_t starts = __ballot_sync(~0u, begins);
+  bool leaves = false;
+  int c0 = 0, blocks = 0;  // of the item that a lane of warp 0 has a part of to leave
+  uint64_t seen = 0;
   if (warp == 0) {
     // the next warps' parts 0, up to one that ends the item or is missing
     const int next = (lane | 1) + 1;
@@ -689,79 +783,83 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     const int steps = stop ? (__ffs(stop) - 1) / 2 : (2 * W - next) / 2;
     const bool last = state == 3 || (next < 32 && ((ends >> next) >> (2 * steps)) & 1);
     const int parts = state == 3 ? 1 : 1 + steps + last;
-    if (begins) groups[__popc(starts & ((1u << lane) - 1))] = make_int4(lane, parts, last, 0);
-    const bool leaves = begins && !((lane & 1) && last);  // never with own blocks
-    const uint32_t left = __ballot_sync(~0u, leaves);
+    leaves = begins && own_blocks == 0 && !((lane & 1) && last);
+    if (begins) groups[__popc(starts & ((1u << lane) - 1))] = lane | parts << 8 | (leaves ? 1u << 16 : 0u);
+    if (lane < 2) closing[lane].y = 0;
     if (leaves) {
-      PartHeader h = hdr[lane >> 1][lane & 1];
-      h.state = last ? 3 : 1;
-      out_hdr[blockIdx.x * 2 + (lane & 1)] = h;
+      const PartHeader& h = hdr[lane >> 1][lane & 1];
+      c0 = (int)(h.start / (span * W));
+      blocks = (int)((h.start + h.cost - 1) / (span * W)) - c0 + 1;
+      seen = *reinterpret_cast<volatile uint64_t*>(counters + c0);
     }
-    if (own_blocks == 0 && lane < 2 && !(left & (lane ? 0xAAAAAAAAu : 0x55555555u))) out_hdr[blockIdx.x * 2 + lane].state = 0;
   }
   __syncthreads();
-  constexpr int E = NT * W_::MT * 32;
-  for (int i = tid; i < __popc(starts) * E; i += 32 * W) {
-    const int4 gr = groups[i / E];
-    const int e = i % E, row = ((e >> 5) / W_::MT) * 8 + 2 * (e & 3);
-    Join join;
-    const int w0 = gr.x >> 1;
-    const P& first = gr.x & 1 ? *reinterpret_cast<const P*>(rings + w0 * kSlot) : heads[w0];
-    join.top(*reinterpret_cast<const float2*>(&first.m[row]));
-#pragma unroll 4
-    for (int c = 1; c < gr.y; ++c) join.top(*reinterpret_cast<const float2*>(&heads[w0 + c].m[row]));
-    join.add(first.o[e], *reinterpret_cast<const float2*>(&first.m[row]), *reinterpret_cast<const float2*>(&first.l[row]));
-#pragma unroll 4
-    for (int c = 1; c < gr.y; ++c) {
-      const P& p = heads[w0 + c];
-      join.add(p.o[e], *reinterpret_cast<const float2*>(&p.m[row]), *reinterpret_cast<const float2*>(&p.l[row]));
+  using J = Words<NT, D>;
+  J join;
+  for (int i = warp; i < __popc(starts) * J::kPieces; i += W) {
+    const uint32_t gr = groups[i / J::kPieces];
+    const int piece = i % J::kPieces, k = gr & 1, w0 = (gr & 0xff) >> 1;
+    const P* first = k ? reinterpret_cast<const P*>(rings + w0 * kSlot) : heads + w0;
+    const float2 top = join.join(piece, lane, gr >> 8 & 0xff, [&](int c) { return c == 0 ? first : heads + w0 + c; });
+    if (gr >> 16) join.leave(out_part + blockIdx.x * 2 + k, piece, lane, top);
+    else join.template write<T>(a, hdr[w0][k], piece, lane);
+  }
+  if (own_blocks > 0) return;
+
+  // The last block to leave a part of an item joins them.
+  __threadfence();
+  __syncthreads();
+  if (leaves) {
+    unsigned long long* at = reinterpret_cast<unsigned long long*>(counters + c0);
+    while (seen >> kCountBits != tag >> kCountBits) {
+      const uint64_t was = atomicCAS(at, seen, tag);
+      seen = was == seen ? tag : was;  // only to the tag does anyone else change it
     }
-    if ((gr.x & 1) && gr.z) {
-      write_merged<T, D, NT>(a, hdr[gr.x >> 1][1], e, join.o, join.l0, join.l1);
-    } else {
-      P* dst = out_part + blockIdx.x * 2 + (gr.x & 1);
-      dst->o[e] = join.o;
-      if ((e >> 5) % W_::MT == 0 && (e & 31) < 4) {
-        *reinterpret_cast<float2*>(&dst->m[row]) = make_float2(join.m0, join.m1);
-        *reinterpret_cast<float2*>(&dst->l[row]) = make_float2(join.l0, join.l1);
-      }
+    if ((int)(atomicAdd(at, 1ull) - tag) + 1 == blocks) {
+      *at = tag;
+      __threadfence();
+      closing[lane & 1] = make_int4(c0, blocks, lane, 0);
     }
   }
-}
-
-// Joins the parts of the items that span blocks: block c those of the item begun in block c of the
-// first kernel.  It is launched while the first one runs and waits for its end.
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(256) combine_kernel(AttnArgs a) {
-  using P = Part<NT, D>;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const PartHeader* hdr = static_cast<const PartHeader*>(a.workspace);
-  const P* part = reinterpret_cast<const P*>(static_cast<const uint8_t*>(a.workspace) + 2 * kCtas * sizeof(PartHeader));
-  const int c0 = blockIdx.x;
-  const PartHeader h = hdr[c0 * 2 + 1];
-  if (h.state != 1) return;
-  const int end = last_part(hdr, c0);
-  for (int e = threadIdx.x; e < NT * D / 16 * 32; e += blockDim.x) {
-    const int row = ((e >> 5) / (D / 16)) * 8 + 2 * (e & 3);
-    Join join;
-#pragma unroll 8
-    for (int c = c0; c <= end; ++c) join.top(*reinterpret_cast<const float2*>(&part[c * 2 + (c == c0)].m[row]));
-#pragma unroll 8
-    for (int c = c0; c <= end; ++c) {
-      const P& p = part[c * 2 + (c == c0)];
-      join.add(p.o[e], *reinterpret_cast<const float2*>(&p.m[row]), *reinterpret_cast<const float2*>(&p.l[row]));
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    const int4 cl = closing[k];
+    if (cl.y == 0) continue;
+    // warps take slices of the parts and a piece each, then a few of them join the slices
+    constexpr int S = W / J::kPieces;
+    static_assert(S >= 2, "");
+    const int piece = warp % J::kPieces, slice = warp / J::kPieces, slices = min(S, cl.y);
+    if (slice < slices) {
+      const int n = (cl.y - slice + S - 1) / S;
+      const float2 top = join.join_far(piece, lane, n, [&](int i) {
+        const int c = slice + i * S;
+        return out_part + (cl.x + c) * 2 + (c == 0);
+      });
+      join.leave(heads + slice, piece, lane, top);
     }
-    write_merged<T, D, NT>(a, h, e, join.o, join.l0, join.l1);
+    __syncthreads();
+    if (slice == 0) {
+      join.join(piece, lane, slices, [&](int c) { return heads + c; });
+      join.template write<T>(a, hdr[cl.z >> 1][cl.z & 1], piece, lane);
+    }
+    __syncthreads();
   }
 }
 
 // Row blocks of a sequence where every item gets a block of its own, or 0.  That is so where the items
-// fit the SMs at once and a warp's share is at most 8 units: no parts leave a block, and the second kernel
-// and the workspace fall away (one sequence of 517 tokens, 8 kv heads: 9.0 us against 11.9; with long
+// fit the SMs at once and a warp's share is at most 8 units: no parts leave a block, and the joins
+// between blocks and the workspace fall away (one sequence of 517 tokens, 8 kv heads: 9.0 us against 11.9; with long
 // contexts ranges over all SMs win).
 int own_blocks(int B, int hkv, int max_q, int r, int64_t capacity, int nt, int warps) {
   const int64_t blocks = ((int64_t)max_q * r + 8 * nt - 1) / (8 * nt);
   return (int64_t)B * hkv * blocks <= kCtas && capacity <= 8 * kUnit * warps ? (int)blocks : 0;
+}
+
+// Of every call another, and none that memory holds by chance: an odd multiple of the call's number.
+uint64_t next_tag() {
+  static std::atomic<uint64_t> calls{0};
+  return (calls.fetch_add(1, std::memory_order_relaxed) + 1) * 0x9E3779B97F4A7C15ull << kCountBits;
 }
 
 template <typename T, int D, int G, int NT>
@@ -784,20 +882,8 @@ cudaError_t launch(const AttnArgs& a, cudaStream_t st) {
   int shift = 4;
   while ((1 << shift) < a.page) ++shift;
   const int r = a.hq / a.hkv, own = own_blocks(a.B, a.hkv, a.max_q, r, (int64_t)a.max_blocks * a.page, NT, W);
-  attn_kernel<T, D, G, NT><<<own ? (unsigned)(a.B * a.hkv * own) : kCtas, 32 * W, bytes, st>>>(a, shift, own);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || own) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas);
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<T, D, NT>, a);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  attn_kernel<T, D, G, NT><<<own ? (unsigned)(a.B * a.hkv * own) : kCtas, 32 * W, bytes, st>>>(a, shift, own, next_tag());
+  return cudaGetLastError();
 }
 
 template <typename T, int D, int G>
@@ -820,7 +906,7 @@ size_t attn_workspace_bytes(int B, int hq, int hkv, int d, int max_q, int64_t ca
   if (rows > kFewRows) return attn_rows_workspace_bytes(d);
   const int nt = rows <= 8 ? 1 : 2, warps = nt == 1 ? kWarpsOf<1, 64> : d == 64 ? kWarpsOf<2, 64> : kWarpsOf<2, 128>;
   if (own_blocks(B, hkv, max_q, hq / hkv, capacity, nt, warps)) return 0;
-  return 2 * kCtas * (sizeof(PartHeader) + (d == 64 ? sizeof(Part<2, 64>) : sizeof(Part<2, 128>)));
+  return kCounters + 2 * kCtas * (d == 64 ? sizeof(Part<2, 64>) : sizeof(Part<2, 128>));
 }
 
 cudaError_t launch_attn(const AttnArgs& a, cudaStream_t st) {

@@ -28,6 +28,24 @@ namespace fq {
 namespace kv4 {
 namespace {
 
+// What a block leaves for the kernel that joins: [kCtas][2] parts, part 0 of an item begun before the
+// block's range, part 1 of an item begun in it that goes on behind it.
+struct PartHeader {
+  int state;             // 0: none, 1: goes on, 3: the item's last part
+  int q0, rows, head, rb;  // where its rows are
+};
+static_assert(2 * kCtas * sizeof(PartHeader) % 16 == 0, "parts behind the headers are read in 16 bytes");
+
+// The block that holds the last part of the item begun in block c0.  All lanes of a warp call it.
+__device__ __forceinline__ int last_part(const PartHeader* hdr, int c0) {
+  const int lane = threadIdx.x & 31;
+  for (int c = c0 + 1; c < kCtas; c += 32) {
+    const uint32_t last = __ballot_sync(~0u, c + lane < kCtas && hdr[(c + lane) * 2].state == 3);
+    if (last) return c + __ffs(last) - 1;
+  }
+  return kCtas - 1;
+}
+
 __device__ unsigned int g_kv4_rows_wait_timeouts = 0;  // blocks whose bounded waits gave up
 
 constexpr int kRows = 128;      // rows of a block's item

@@ -360,6 +360,46 @@ def test_another_stream_with_no_wait_for_the_default_one():
     assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("qlens", [None, [3, 1, 0, 4, 2], [11, 4, 0, 1, 2]])
+def test_a_workspace_of_any_content_serves_call_after_call_and_graphs_in_turn(qlens):
+    rng = np.random.default_rng(18)
+    c = Cache(rng, [5000, 37, 0, 2100, 700], 2, 64, 32, 16)
+    one = Cache(rng, [9000], 1, 128, 64, 64)  # one kv head: every block has a part of the only item
+    qlens1 = None if qlens is None else [max(qlens)]
+    need = max(fq.fq_kv4_attn_workspace_bytes(len(x.lens), 8 * x.hkv, x.hkv, x.d, 1 if qlens is None else max(qlens),
+                                              x.tables.shape[1], x.page) for x in (c, one))
+    assert need > 0
+    calls = []
+    for x, m in ((c, qlens), (one, qlens1)):
+        q = _q(rng, len(x.lens) if m is None else sum(m), 8 * x.hkv, x.d, torch.float16)
+        cu = None if m is None else _dev(np.concatenate([[0], np.cumsum(m)]).astype(np.int32))
+        lens = _dev(x.lens)
+        kw = dict(cu_q=cu, max_q=1 if m is None else max(m))
+        calls.append((q, _dev(x.host), _dev(x.tables), lens, x.group, kw, torch.empty_like(q)))
+        _attend(x, q, m)
+    want = [[fq.fq_kv4_attn(q, pool, t, n - k, g, **kw) for k in (0, 8, 3)] for q, pool, t, n, g, kw, _ in calls]
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    for fill in (0, 1, 0x7F, 0xFF, None):
+        ws.copy_(torch.randint(0, 256, (need,), dtype=torch.uint8)) if fill is None else ws.fill_(fill)
+        for i in (0, 1, 1, 0):
+            q, pool, t, n, g, kw, out = calls[i]
+            assert torch.equal(fq.fq_kv4_attn(q, pool, t, n, g, out=out.fill_(7), workspace=ws, **kw), want[i][0])
+    graphs = []
+    torch.cuda.synchronize()
+    for q, pool, t, n, g, kw, out in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            fq.fq_kv4_attn(q, pool, t, n, g, out=out, workspace=ws, **kw)
+    ws.fill_(0xA5)
+    for k, i in ((0, 0), (0, 0), (0, 1), (1, 0), (1, 1), (2, 1), (2, 0), (0, 1), (0, 0)):
+        q, pool, t, n, g, kw, out = calls[i]
+        n.sub_((0, 8, 3)[k])  # a replay reads the lengths that are there then
+        out.fill_(7)
+        graphs[i].replay()
+        assert torch.equal(out, want[i][k])
+        n.add_((0, 8, 3)[k])
+
+
 def test_binding_refuses_wrong_tensors():
     rng = np.random.default_rng(17)
     c = Cache(rng, [20, 20], 2, 64, 32, 16)
