@@ -54,7 +54,9 @@ constexpr int kTileUnits = kTile / kUnit;
 constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
 constexpr int kSoftmaxWarps = 8;  // warps w and w + 4 share 32 rows, 64 columns each
 constexpr int kKeyWarps = 4, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueWarps;
-constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 4;  // mma, two loaders, one idle: whole warpgroups
+constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 4;  // two for the products, two loaders
+// units of a stage of a ring: a loader's step takes ~700 cycles and ~85 more for each copy
+constexpr int kChunkUnits = 4;
 // registers a thread: 96 at launch, 20 warps x 96 = 8 x 144 + 12 x 64
 constexpr int kSoftmaxRegs = 144, kOtherRegs = 64;
 
@@ -70,18 +72,22 @@ struct Shape {
   static constexpr int kOp = kTile * D * 2;          // bytes of one fp16 operand of a tile
   static constexpr int kZ = EXACT ? kTile * 32 : 0;  // zeros: 16 numbers a token
   static constexpr int kK = (EXACT ? 2 : 1) * kOp + kZ, kBuf = kK + kOp;
-  static constexpr int kChunkUnits = D == 128 ? 2 : 4;  // units of a ring's stage: one step of 4 warps
-  static constexpr int kChunks = kTileUnits / kChunkUnits, kCodes = kChunkUnits * kUnit * D / 2, kPacked = kCodes + kChunkUnits * 64 * NG;
-  static constexpr int kRing = EXACT && D == 128 ? 4 : 8;  // what shared memory leaves
+  static constexpr int kChunks = kTileUnits / kChunkUnits, kCodes = kUnit * D / 2, kScales = 64 * NG;
+  // a stage of the keys' ring: codes of its units, then steps and zeros; of the values': codes, the keys'
+  // steps and zeros, which lie between, and their own of a unit in one piece
+  static constexpr int kKeys = kChunkUnits * (kCodes + kScales), kValue = kCodes + 2 * kScales, kValues = kChunkUnits * kValue;
+  static constexpr int kRing = D == 64 ? 8 : EXACT ? 2 : 4;  // what shared memory leaves
   static constexpr size_t kControl = 1024;
-  static constexpr size_t kSmem = kControl + 2 * kBuf + 2 * kRing * kPacked;
+  static constexpr size_t kSmem = kControl + 2 * kBuf + kRing * (kKeys + kValues);
   // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
   static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
 
 struct Control {
   uint64_t ring_full[2][8], ring_empty[2][8];  // keys, values
-  uint64_t k_full[2], v_full[2], pv_done[2], s_full[2], p_full[2], q_full;
+  // scores may be computed: keys are there, and the weights in their place used up; are computed;
+  // values and weights are there; are used up
+  uint64_t s_ready[2], s_full[2], pv_ready[2], pv_done[2], q_full;
   uint32_t tmem;
   int gave_up;
   int gone[2][8];  // units of the last eight tiles that are not there (bits), by each loader
@@ -171,12 +177,9 @@ __device__ __forceinline__ void codes(uint32_t w, __half2 (&c)[4]) {
 // words) of a token.  Rows go K-major with the 128-byte swizzle; lanes are spread so that no eight of
 // them meet in a bank.
 template <int D, int G, bool EXACT>
-__device__ __forceinline__ void unpack_keys(uint32_t codes_at, uint32_t scales_at, uint32_t buf, int place, int ch, int row_unit) {
+__device__ __forceinline__ void unpack_keys(const uint32_t (&w)[4], const uint32_t (&sc)[D / G], uint32_t buf, int place, int ch, int row_unit) {
   using C = Shape<D, G, EXACT>;
-  uint32_t w[4], sc[C::NG];
   // packed row `place` holds token 0 4 1 5 2 6 3 7 (+ 8)
-  lds<16>(codes_at + place * (D / 2) + ch * 16, w);
-  lds<4 * C::NG>(scales_at + place * 4 * C::NG, sc);
   const int n = row_unit + (place >> 1 & 3) + 4 * (place & 1) + (place & 8);
   const uint32_t krow = buf + n * 128;
 #pragma unroll
@@ -206,14 +209,17 @@ __device__ __forceinline__ void unpack_keys(uint32_t codes_at, uint32_t scales_a
   }
 }
 
+// Which 32 coordinates a chunk of packed values holds.
+template <int D>
+__device__ __forceinline__ int value_group(int place, int ch) {
+  return D == 128 ? ch ^ (place & 2) : ch;
+}
+
 // The same of values: rows go MN-major.  seen: somebody sees the token; its values are 0 otherwise.
 template <int D, int G, bool EXACT>
-__device__ __forceinline__ void unpack_values(uint32_t codes_at, uint32_t scales_at, uint32_t buf, int place, int ch, int row, bool seen) {
+__device__ __forceinline__ void unpack_values(uint32_t (&w)[4], uint32_t sz, uint32_t buf, int place, int ch, int row, bool seen) {
   using C = Shape<D, G, EXACT>;
-  uint32_t w[4], sz;
-  lds<16>(codes_at + place * (D / 2) + ch * 16, w);
-  const int group = D == 128 ? ch ^ (place & 2) : ch;  // 32 coordinates
-  lds<4>(scales_at + (place * C::NG + group * 32 / G) * 4, &sz);
+  const int group = value_group<D>(place, ch);
   if (!seen) sz = 0;
   if (D == 128 && (group & 2)) {
     uint32_t x = w[0]; w[0] = w[2]; w[2] = x;
@@ -233,6 +239,14 @@ __device__ __forceinline__ void unpack_values(uint32_t codes_at, uint32_t scales
 
 // ------------------------------------------------------------------------------ the kernel
 
+// An operand's descriptor `bytes` further on.  One addition: one thread issues a tile's products one
+// after another, and whatever it computes between them is time of the tensor pipe's.
+__device__ __forceinline__ uint64_t moved(uint64_t desc, uint32_t bytes) {
+  uint64_t y;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "r"((uint32_t)desc + bytes / 16), "r"((uint32_t)(desc >> 32)));
+  return y;
+}
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int page_shift) {
   constexpr bool kExact = __is_same(T, __half);
@@ -250,18 +264,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     ctl.gave_up = 0;
     for (int i = 0; i < kRing; ++i) {
       for (int k = 0; k < 2; ++k) {
-        ptx::mbar_init(&ctl.ring_full[k][i], C::kChunkUnits);
+        ptx::mbar_init(&ctl.ring_full[k][i], kChunkUnits);
         ptx::mbar_init(&ctl.ring_empty[k][i], 4);
       }
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&ctl.k_full[i], kKeyWarps);
-      ptx::mbar_init(&ctl.v_full[i], kValueWarps);
-      ptx::mbar_init(&ctl.pv_done[i], 1);
+      ptx::mbar_init(&ctl.s_ready[i], kKeyWarps + 1);
+      ptx::mbar_arrive(&ctl.s_ready[i]);  // no weights before the first two tiles
       ptx::mbar_init(&ctl.s_full[i], 1);
-      ptx::mbar_init(&ctl.p_full[i], kSoftmaxWarps);
+      ptx::mbar_init(&ctl.pv_ready[i], kValueWarps + kSoftmaxWarps);
+      ptx::mbar_init(&ctl.pv_done[i], 1);
     }
-    ptx::mbar_init(&ctl.q_full, 4);
+    ptx::mbar_init(&ctl.q_full, kSoftmaxWarps);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -364,29 +378,33 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       const uint32_t last_row = min(it.rb * kRows + kRows, it.s.rows) - 1;
       const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? hi - a.window : 0;
       if (it.t0 < it.t1) {
-        // this thread's row of q, by a power of two in fp16, its keys' order of coordinates
-        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(it.s.q0 + tok) * a.q_tok + (int64_t)(it.head * r + hh) * a.q_head;
+        // this thread's half row of q, by a power of two in fp16, its keys' order of coordinates
+        const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(it.s.q0 + tok) * a.q_tok + (int64_t)(it.head * r + hh) * a.q_head + half * (D / 2);
         const bool wide = reinterpret_cast<uintptr_t>(src) % 16 == 0;
-        auto word = [&](int w) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (!in) return v;
-          const uint16_t* p = src + 8 * w;
-          if (wide) return __ldg(reinterpret_cast<const uint4*>(p));
-          v.x = __ldg(p) | (uint32_t)__ldg(p + 1) << 16;
-          v.y = __ldg(p + 2) | (uint32_t)__ldg(p + 3) << 16;
-          v.z = __ldg(p + 4) | (uint32_t)__ldg(p + 5) << 16;
-          v.w = __ldg(p + 6) | (uint32_t)__ldg(p + 7) << 16;
-          return v;
-        };
-        float top = 0.f;
-#pragma unroll 4
-        for (int w = 0; w < D / 8; ++w) {
-          const uint4 v = word(w);
-          const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+        uint32_t q[D / 4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            top = fmaxf(top, fmaxf(fabsf(q_float<T>((uint16_t)x[i])), fabsf(q_float<T>((uint16_t)(x[i] >> 16)))));
+        for (int w = 0; w < D / 16; ++w) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          const uint16_t* p = src + 8 * w;
+          if (in && wide) {
+            v = __ldg(reinterpret_cast<const uint4*>(p));
+          } else if (in) {
+            v.x = __ldg(p) | (uint32_t)__ldg(p + 1) << 16;
+            v.y = __ldg(p + 2) | (uint32_t)__ldg(p + 3) << 16;
+            v.z = __ldg(p + 4) | (uint32_t)__ldg(p + 5) << 16;
+            v.w = __ldg(p + 6) | (uint32_t)__ldg(p + 7) << 16;
+          }
+          q[4 * w] = v.x;
+          q[4 * w + 1] = v.y;
+          q[4 * w + 2] = v.z;
+          q[4 * w + 3] = v.w;
         }
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i)
+          top = fmaxf(top, fmaxf(fabsf(q_float<T>((uint16_t)q[i])), fabsf(q_float<T>((uint16_t)(q[i] >> 16)))));
+        meet(top);
+        top = fmaxf(top, theirs());
         const int e = top > 0.f ? max((int)(__float_as_uint(top) >> 23) - 134, -126) : 0;
         float down = __uint_as_float((uint32_t)(127 - e) << 23);
         kappa = a.scale * 1.4426950408889634f * __uint_as_float((uint32_t)(127 + e) << 23);
@@ -395,36 +413,40 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           down = -down;
         }
         kappa = fmaxf(kappa, 1e-37f);  // so that -inf, a masked score, stays that
-        if (half == 0) {
-          float sum[C::NG];
+        constexpr int kSums = C::NG > 1 ? C::NG / 2 : 1;  // groups of half a row
+        float sum[kSums];
 #pragma unroll
-          for (int i = 0; i < C::NG; ++i) sum[i] = 0.f;
+        for (int i = 0; i < kSums; ++i) sum[i] = 0.f;
 #pragma unroll
-          for (int w4 = 0; w4 < D / 8; w4 += 4) {  // 32 coordinates: 16 columns
-            uint32_t col[16];
+        for (int w = 0; w < D / 16; ++w) {
+          __half y[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 v = word(w4 + i);
-              const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-              __half y[8];
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                y[k] = __float2half_rn(q_float<T>((uint16_t)(x[k / 2] >> (16 * (k & 1)))) * down);
-                sum[8 * w4 / G] += __half2float(y[k]);
-              }
-#pragma unroll
-              for (int k = 0; k < 4; ++k) col[4 * i + k] = u32(__halves2half2(y[k], y[k + 4]));
-            }
-            __syncwarp();
-            ptx::tmem_st16(lanes + C::Q + 4 * w4, col);
+          for (int k = 0; k < 8; ++k) {
+            y[k] = __float2half_rn(q_float<T>((uint16_t)(q[4 * w + k / 2] >> (16 * (k & 1)))) * down);
+            if (kExact) sum[C::NG > 1 ? 8 * w / G : 0] += __half2float(y[k]);
           }
-          if (kExact) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q[4 * w + k] = u32(__halves2half2(y[k], y[k + 4]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < D / 4; c += 16) ptx::tmem_st16(lanes + C::Q + half * (D / 4) + c, *reinterpret_cast<uint32_t(*)[16]>(q + c));
+        if (kExact) {
+          float all[2 * kSums];
+#pragma unroll
+          for (int i = 0; i < kSums; ++i) {
+            meet(sum[i]);
+            all[i] = sum[i];
+            all[kSums + i] = theirs();
+          }
+          if (half == 0) {
+            if (C::NG == 1) all[0] += all[1];
             uint32_t qz[8] = {0, 0, 0, 0, 0, 0, 0, 0};
             __half part[2][C::NG];
 #pragma unroll
             for (int i = 0; i < C::NG; ++i) {
-              part[0][i] = __float2half_rn(sum[i]);
-              part[1][i] = __float2half_rn(sum[i] - __half2float(part[0][i]));
+              part[0][i] = __float2half_rn(all[i]);
+              part[1][i] = __float2half_rn(all[i] - __half2float(part[0][i]));
             }
             if constexpr (C::NG == 1) {
               qz[0] = u32(__halves2half2(part[0][0], part[1][0]));
@@ -436,11 +458,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
             }
             ptx::tmem_st8(lanes + C::QZ, qz);
           }
-          ptx::tmem_wait_st();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
         }
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
 
         for (int j = it.t0; j < it.t1; ++j, ++tile) {
           const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf;
@@ -509,7 +531,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           ptx::tmem_wait_st();
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&ctl.p_full[buf]);
+          if (lane == 0) ptx::mbar_arrive(&ctl.pv_ready[buf]);
         }
         all_wait(&ctl.pv_done[(tile - 1) & 1], (tile - 1) >> 1);
         meet(l);
@@ -522,27 +544,27 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
       T* dst = static_cast<T*>(a.out) + ((int64_t)(it.s.q0 + tok) * a.hq + it.head * r + hh) * D;
 #pragma unroll 1
-      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-        uint32_t o[16];
+      for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        uint32_t o[32];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = 0;
+        for (int i = 0; i < 32; ++i) o[i] = 0;
         __syncwarp();
         if (any) {
-          ptx::tmem_ld16(lanes + C::O + c, o);
+          ptx::tmem_ld_cols<0, 32>(lanes + C::O + c, o);
           ptx::tmem_wait_ld();
         }
         if (!in) continue;
-        float v[16];  // columns are coordinates 0 4 1 5 2 6 3 7 of each eight
+        float v[32];  // columns are coordinates 0 4 1 5 2 6 3 7 of each eight
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[(i & 8) + (i >> 1 & 3) + 4 * (i & 1)] = __uint_as_float(o[i]);
+        for (int i = 0; i < 32; ++i) v[(i & 24) + (i >> 1 & 3) + 4 * (i & 1)] = __uint_as_float(o[i]);
         if (whole) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 8)
+          for (int i = 0; i < 32; i += 8)
             *reinterpret_cast<uint4*>(dst + c + i) = make_uint4(pack_out<T>(v[i] * inv, v[i + 1] * inv), pack_out<T>(v[i + 2] * inv, v[i + 3] * inv),
                                                                 pack_out<T>(v[i + 4] * inv, v[i + 5] * inv), pack_out<T>(v[i + 6] * inv, v[i + 7] * inv));
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4*>(&part->o[my_row][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(&part->o[my_row][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
       if (!whole) {
@@ -575,125 +597,146 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           const uint32_t slot = chunk % kRing;
           wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
           __syncwarp();
-          const uint32_t at = packed32 + ((keys ? 0 : kRing) + slot) * C::kPacked;
-          const int row0 = c * C::kChunkUnits * kUnit, in_chunk = (warp & 3) * kStep + row_lane, row = row0 + in_chunk;  // of the tile
-          const uint32_t codes_at = at + in_chunk / kUnit * (kUnit * D / 2), scales_at = at + C::kCodes + in_chunk / kUnit * (64 * C::NG);
-          if (keys) {
-            unpack_keys<D, G, kExact>(codes_at, scales_at, base, row % kUnit, ch, row & ~(kUnit - 1));
-          } else {
-            const int pos = it.base_u * kUnit + j * kTile + row, gone = *(volatile int*)&ctl.gone[1][tile & 7];
-            unpack_values<D, G, kExact>(codes_at, scales_at, base + C::kK, row % kUnit, ch, row,
-                                        pos >= it.first && pos < it.end && !(gone >> (row / kUnit) & 1));
+          const uint32_t at = packed32 + (keys ? slot * C::kKeys : kRing * C::kKeys + slot * C::kValues);
+          // all reads of the stage come first: it is free again while its tokens are unpacked
+          constexpr int kSteps = kChunkUnits * kUnit / (4 * kStep);
+          uint32_t w[kSteps][4], sc[kSteps][C::NG];
+          const int row0 = (warp & 3) * kStep + row_lane, place = row0 % kUnit;
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int unit = (4 * i * kStep + row0) / kUnit;
+            const uint32_t codes_at = at + unit * (keys ? C::kCodes : C::kValue);
+            lds<16>(codes_at + place * (D / 2) + ch * 16, w[i]);
+            if (keys) lds<4 * C::NG>(at + kChunkUnits * C::kCodes + unit * C::kScales + place * 4 * C::NG, sc[i]);
+            else lds<4>(codes_at + C::kCodes + C::kScales + (place * C::NG + value_group<D>(place, ch) * 32 / G) * 4, sc[i]);
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl.ring_empty[!keys][slot]);
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const int row = c * kChunkUnits * kUnit + 4 * i * kStep + row0;  // of the tile
+            if (keys) {
+              unpack_keys<D, G, kExact>(w[i], sc[i], base, place, ch, row & ~(kUnit - 1));
+            } else {
+              const int pos = it.base_u * kUnit + j * kTile + row, gone = *(volatile int*)&ctl.gone[1][tile & 7];
+              unpack_values<D, G, kExact>(w[i], sc[i][0], base + C::kK, place, ch, row,
+                                          pos >= it.first && pos < it.end && !(gone >> (row / kUnit) & 1));
+            }
+          }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(keys ? &ctl.k_full[buf] : &ctl.v_full[buf]);
+        if (lane == 0) ptx::mbar_arrive(keys ? &ctl.s_ready[buf] : &ctl.pv_ready[buf]);
       }
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
     if (warp == kSoftmaxWarps + kUnpackWarps) {
-    // ---------------------------------------------------------------- mma
-    constexpr uint32_t idesc_s = ptx::idesc_f16_f32(128, kTile), idesc_o = ptx::idesc_f16_f32(128, D) | (1u << 16);
-    bool ok = true;
-    uint32_t item = 0;
-    auto scores = [&](uint32_t t) {  // S of tile t
-      const uint32_t buf = t & 1, base = smem32 + buf * C::kBuf, d = tmem + C::S + 128 * buf;
-#pragma unroll
-      for (int part = 0; part < (kExact ? 2 : 1); ++part)
-#pragma unroll
-        for (int ks = 0; ks < D / 16; ++ks)
-          ptx::umma_f16_ts(d, tmem + C::Q + 8 * ks, ptx::sdesc_kmajor_sw128(base + part * C::kOp + (ks >> 2) * (kTile * 128) + (ks & 3) * 32),
-                           idesc_s, part > 0 || ks > 0 ? 1u : 0u);
-      if (kExact) ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 2 * C::kOp, 128, 256), idesc_s, 1u);
-      ptx::umma_commit(&ctl.s_full[buf]);
-    };
-    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
-      if (it.t0 >= it.t1) continue;
-      if (lane == 0) {
-        ok = wait(&ctl, &ctl.q_full, item) && wait(&ctl, &ctl.k_full[tile & 1], tile >> 1);
-        if (ok) {
-          ptx::tc_fence_after();
-          scores(tile);
-        }
-        for (int j = it.t0; j < it.t1 && ok; ++j) {
-          const uint32_t t = tile + (j - it.t0), buf = t & 1;
-          if (j + 1 < it.t1) {
-            // the next tile's scores take the place of the weights of the tile before
-            ok = wait(&ctl, &ctl.k_full[buf ^ 1], (t + 1) >> 1) && (t == 0 || wait(&ctl, &ctl.pv_done[buf ^ 1], (t - 1) >> 1));
+      // ---------------------------------------------------------------- scores
+      constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile);
+      bool ok = true;
+      uint32_t item = 0;
+      for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+        const int tiles = it.t1 - it.t0;
+        if (tiles <= 0) continue;
+        if (lane == 0) {
+          ok = wait(&ctl, &ctl.q_full, item);
+          for (uint32_t t = tile; t < tile + tiles && ok; ++t) {
+            const uint32_t buf = t & 1, base = smem32 + buf * C::kBuf, d = tmem + C::S + 128 * buf;
+            ok = wait(&ctl, &ctl.s_ready[buf], t >> 1);
             if (!ok) break;
             ptx::tc_fence_after();
-            scores(t + 1);
+            const uint64_t keys = ptx::sdesc_kmajor_sw128(base);
+#pragma unroll
+            for (int part = 0; part < (kExact ? 2 : 1); ++part)
+#pragma unroll
+              for (int ks = 0; ks < D / 16; ++ks)
+                ptx::umma_f16_ts(d, tmem + C::Q + 8 * ks, moved(keys, part * C::kOp + (ks >> 2) * (kTile * 128) + (ks & 3) * 32), idesc,
+                                 part > 0 || ks > 0 ? 1u : 0u);
+            if (kExact) ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 2 * C::kOp, 128, 256), idesc, 1u);
+            ptx::umma_commit(&ctl.s_full[buf]);
           }
-          ok = wait(&ctl, &ctl.v_full[buf], t >> 1) && wait(&ctl, &ctl.p_full[buf], t >> 1);
+        }
+        ok = __shfl_sync(~0u, (int)ok, 0);
+        tile += tiles;
+        ++item;
+      }
+    } else if (warp == kSoftmaxWarps + kUnpackWarps + 1) {
+      // ---------------------------------------------------------------- weighted values
+      constexpr uint32_t idesc = ptx::idesc_f16_f32(128, D) | (1u << 16);
+      bool ok = true;
+      for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+        const int tiles = it.t1 - it.t0;
+        if (lane == 0)
+          for (uint32_t t = tile; t < tile + tiles; ++t) {
+            const uint32_t buf = t & 1, weights = tmem + C::S + 128 * buf;
+            ok = wait(&ctl, &ctl.pv_ready[buf], t >> 1);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            const uint64_t values = ptx::sdesc_mnmajor_sw128(smem32 + buf * C::kBuf + C::kK, 1024, C::NA * 1024);
+#pragma unroll
+            for (int part = 0; part < (kExact ? 2 : 1); ++part)
+#pragma unroll
+              for (int ks = 0; ks < kTile / 16; ++ks)
+                ptx::umma_f16_ts(tmem + C::O, weights + 64 * part + 8 * ks, moved(values, ks * 2 * C::NA * 1024), idesc,
+                                 t > tile || part > 0 || ks > 0 ? 1u : 0u);
+            ptx::umma_commit(&ctl.pv_done[buf]);
+            ptx::umma_commit(&ctl.s_ready[buf]);
+          }
+        ok = __shfl_sync(~0u, (int)ok, 0);
+        tile += max(tiles, 0);
+      }
+    } else {
+      // ---------------------------------------------------------------- loaders
+      const bool keys = warp == kSoftmaxWarps + kUnpackWarps + 2;
+      const int ring = keys ? 0 : 1, stage = keys ? C::kKeys : C::kValues;
+      const uint8_t* cache = a.cache + (keys ? 0 : C::kCodes);
+      // where lane i's unit of a stage goes: lanes at .. at + 3 copy its four units
+      uint8_t* dst = packed + (keys ? (lane % kChunkUnits) * C::kCodes : kRing * C::kKeys + (lane % kChunkUnits) * C::kValue);
+      bool ok = true;
+      const int shift = page_shift - 4;
+      uint32_t chunk = 0;
+      for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
+        const int32_t* table = a.tables + (int64_t)it.b * a.max_blocks;
+        const int u_begin = it.base_u + it.t0 * kTileUnits, u_end = min(it.base_u + it.t1 * kTileUnits, (it.end + kUnit - 1) / kUnit);
+        auto entry = [&](int u) { return u < u_end ? __ldg(table + (u >> shift)) : -1; };
+        // lane i holds the table entry of units i, i + 32, ... of the part; the next 32 are on their way
+        int id_next = it.t0 < it.t1 ? entry(u_begin + lane) : -1;
+        const uint8_t* src = nullptr;
+        uint32_t there = 0;
+        for (int j = 0; j < (it.t1 - it.t0) * C::kChunks; ++j, ++chunk) {
+          const int at = (j * kChunkUnits) & 31;
+          if (at == 0) {
+            const int id = id_next, u = u_begin + j * kChunkUnits + lane;
+            id_next = entry(u + 32);
+            there = __ballot_sync(~0u, id >= 0 && id < a.n_blocks);
+            src = cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
+          }
+          const uint32_t slot = chunk % kRing;
+          if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[ring][slot], chunk / kRing - 1));
           if (!ok) break;
-          ptx::tc_fence_after();
-          const uint32_t v = smem32 + buf * C::kBuf + C::kK;
-#pragma unroll
-          for (int part = 0; part < (kExact ? 2 : 1); ++part)
-#pragma unroll
-            for (int ks = 0; ks < kTile / 16; ++ks)
-              ptx::umma_f16_ts(tmem + C::O, tmem + C::S + 128 * buf + 64 * part + 8 * ks,
-                               ptx::sdesc_mnmajor_sw128(v + ks * 2 * C::NA * 1024, 1024, C::NA * 1024), idesc_o,
-                               j > it.t0 || part > 0 || ks > 0 ? 1u : 0u);
-          ptx::umma_commit(&ctl.pv_done[buf]);
-        }
-      }
-      ok = __shfl_sync(~0u, (int)ok, 0);
-      tile += it.t1 - it.t0;
-      ++item;
-    }
-    } else if (warp < kSoftmaxWarps + kUnpackWarps + 3) {
-    // ---------------------------------------------------------------- loaders
-    const int kind = warp - (kSoftmaxWarps + kUnpackWarps + 1);  // keys, values
-    bool ok = true;
-    const int shift = page_shift - 4;
-    uint32_t chunk = 0;
-    for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
-      const int32_t* table = a.tables + (int64_t)it.b * a.max_blocks;
-      const int u_begin = it.base_u + it.t0 * kTileUnits, u_end = min(it.base_u + it.t1 * kTileUnits, (it.end + kUnit - 1) / kUnit);
-      auto entry = [&](int u) { return u < u_end ? __ldg(table + (u >> shift)) : -1; };
-      // lane i holds the table entry of units i, i + 32, ... of the part; the next 32 are on their way
-      int id = -1, id_next = it.t0 < it.t1 ? entry(u_begin + lane) : -1;
-      for (int j = 0; j < (it.t1 - it.t0) * C::kChunks; ++j, ++chunk) {
-        const int at = (j * C::kChunkUnits) & 31;
-        if (at == 0) {
-          id = id_next;
-          id_next = entry(u_begin + j * C::kChunkUnits + 32 + lane);
-        }
-        const uint32_t slot = chunk % kRing;
-        if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[kind][slot], chunk / kRing - 1));
-        if (!ok) break;
-        const bool good = id >= 0 && id < a.n_blocks;
-        const uint32_t there = __ballot_sync(~0u, good) >> (at & ~(kTileUnits - 1));
-        // A tile's first chunk brings its mask.  The place is free: a ring holds two tiles at most, the keys
-        // of the tile two back are unpacked when the scores of the one four back are done, these come after
-        // the weights of the one six back, and the softmax is past the one eight back.
-        if (j % C::kChunks == 0 && lane == at) *(volatile int*)&ctl.gone[kind][(chunk / C::kChunks) & 7] = ~there & ((1 << kTileUnits) - 1);
-        __syncwarp();
-        const int i = lane - at;
-        if ((unsigned)i < C::kChunkUnits) {
-          if (good) {
-            const int u = u_begin + j * C::kChunkUnits + i;
-            const uint8_t* src = a.cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
-            uint8_t* dst = packed + (kind * kRing + slot) * C::kPacked;
-            constexpr int kCodes = kUnit * D / 2, kScales = 64 * C::NG;
-            ptx::mbar_arrive_expect_tx(&ctl.ring_full[kind][slot], kCodes + kScales);
-            ptx::bulk_load(dst + i * kCodes, src + kind * kCodes, kCodes, &ctl.ring_full[kind][slot]);
-            ptx::bulk_load(dst + C::kCodes + i * kScales, src + 2 * kCodes + kind * kScales, kScales, &ctl.ring_full[kind][slot]);
-          } else {
-            ptx::mbar_arrive(&ctl.ring_full[kind][slot]);
+          if (lane / kChunkUnits == at / kChunkUnits) {
+            uint64_t* bar = &ctl.ring_full[ring][slot];
+            // A tile's first chunk brings its mask.  The place is free: a ring holds four tiles at most, the keys
+            // of the tile four back are unpacked when the scores of the one six back are done, and these come
+            // after the weighted values of the one eight back.
+            if (j % C::kChunks == 0 && lane == at)
+              *(volatile int*)&ctl.gone[ring][(chunk / C::kChunks) & 7] = ~(there >> (at & ~(kTileUnits - 1))) & ((1 << kTileUnits) - 1);
+            if (there >> lane & 1) {
+              ptx::mbar_arrive_expect_tx(bar, keys ? C::kCodes + C::kScales : C::kValue);
+              ptx::bulk_load(dst + slot * stage, src, keys ? C::kCodes : C::kValue, bar);
+              if (keys)
+                ptx::bulk_load(packed + slot * stage + kChunkUnits * C::kCodes + (lane % kChunkUnits) * C::kScales, src + 2 * C::kCodes, C::kScales, bar);
+            } else {
+              ptx::mbar_arrive(bar);
+            }
           }
+          __syncwarp();
         }
-        __syncwarp();
       }
-    }
-    // copies in flight land before the block ends, also where a wait gave up
-    if (!ok)
-      for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[kind][t % kRing], (t / kRing) & 1);
+      // copies in flight land before the block ends, also where a wait gave up
+      if (!ok)
+        for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[ring][t % kRing], (t / kRing) & 1);
     }
   }
 
@@ -702,8 +745,10 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
   ptx::tc_fence_after();
   if (ctl.gave_up && warp == 0) {
     // products that may be in flight: the last ones were committed to these
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      for (uint32_t n = 0; n < 4096 && !ptx::mbar_try(&ctl.s_full[i], 0) && !ptx::mbar_try(&ctl.s_full[i], 1); ++n) {}
       for (uint32_t n = 0; n < 4096 && !ptx::mbar_try(&ctl.pv_done[i], 0) && !ptx::mbar_try(&ctl.pv_done[i], 1); ++n) {}
+    }
     if (lane == 0) atomicAdd(&g_kv4_rows_wait_timeouts, 1u);
   }
   if (warp == 0) ptx::tmem_dealloc(tmem, 512);
