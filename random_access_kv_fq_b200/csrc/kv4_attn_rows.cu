@@ -57,8 +57,8 @@ constexpr int kKeyWarps = 4, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueW
 constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 4;  // two for the products, two loaders
 // units of a stage of a ring: a loader's step takes ~700 cycles and ~85 more for each copy
 constexpr int kChunkUnits = 4;
-// registers a thread: 96 at launch, 20 warps x 96 = 8 x 144 + 12 x 64
-constexpr int kSoftmaxRegs = 144, kOtherRegs = 64;
+// registers a thread: 96 at launch, 20 warps x 96 >= 8 x 128 + 12 x 72; nothing is spilled
+constexpr int kSoftmaxRegs = 128, kOtherRegs = 72;
 
 template <int D>
 struct RowsPart {
@@ -78,7 +78,8 @@ struct Shape {
   static constexpr int kKeys = kChunkUnits * (kCodes + kScales), kValue = kCodes + 2 * kScales, kValues = kChunkUnits * kValue;
   static constexpr int kRing = D == 64 ? 8 : EXACT ? 2 : 4;  // what shared memory leaves
   static constexpr size_t kControl = 1024;
-  static constexpr size_t kSmem = kControl + 2 * kBuf + kRing * (kKeys + kValues);
+  static constexpr size_t kItems = kControl + 2 * kBuf + kRing * (kKeys + kValues);
+  static constexpr size_t kSmem = kItems + kWarps * 80;
   // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
   static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
@@ -115,7 +116,8 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }
 enum { kBarSoftmax = 1, kBarPair = 2 };
 
-// The items of a block's range of the line, one at a time, the same in every role.
+// The items of a block's range of the line, one at a time, the same in every role.  Each warp has its own
+// in shared memory: in registers they would be spilled.
 template <int D>
 struct Items {
   int64_t left;
@@ -124,35 +126,41 @@ struct Items {
   // of the current item
   int to, rb, end, first, base_u, t0, t1, past;
   __device__ __forceinline__ bool next(const AttnArgs& a, int r, bool begun) {
+    __syncwarp();
+    Items x = *this;
+    __syncwarp();
     if (begun) {
-      from = 0;
-      if (left > 0 && ++block == s.blocks) {
-        block = 0;
-        if (++head == a.hkv) {
-          head = 0;
-          do s = load_seq<kRows, kTile, kItemTiles>(a, ++b, r); while (s.blocks == 0);
+      x.from = 0;
+      if (x.left > 0 && ++x.block == x.s.blocks) {
+        x.block = 0;
+        if (++x.head == a.hkv) {
+          x.head = 0;
+          do x.s = load_seq<kRows, kTile, kItemTiles>(a, ++x.b, r); while (x.s.blocks == 0);
         }
       }
     }
-    if (left <= 0) return false;
-    to = (int)min((int64_t)s.cost, from + left);
-    left -= to - from;
+    if (x.left <= 0) return false;
+    const Seq& s = x.s;
+    x.to = (int)min((int64_t)s.cost, x.from + x.left);
+    x.left -= x.to - x.from;
     // row blocks from both ends in turn: two neighbours see about as many tokens as any two
-    rb = block & 1 ? s.blocks - 1 - (block >> 1) : block >> 1;
-    past = s.n - s.m + 1;
-    const uint32_t row0 = rb * kRows, row1 = min(rb * kRows + kRows, s.rows) - 1;
-    end = max(0, past + (int)(row1 / (uint32_t)r));
-    first = a.window > 0 ? max(0, past + (int)(row0 / (uint32_t)r) - a.window) : 0;
-    base_u = first / kUnit;
-    const int tiles = end > first ? (end - base_u * kUnit + kTile - 1) / kTile : 0;
+    x.rb = x.block & 1 ? s.blocks - 1 - (x.block >> 1) : x.block >> 1;
+    x.past = s.n - s.m + 1;
+    const uint32_t row0 = x.rb * kRows, row1 = min(x.rb * kRows + kRows, s.rows) - 1;
+    x.end = max(0, x.past + (int)(row1 / (uint32_t)r));
+    x.first = a.window > 0 ? max(0, x.past + (int)(row0 / (uint32_t)r) - a.window) : 0;
+    x.base_u = x.first / kUnit;
+    const int tiles = x.end > x.first ? (x.end - x.base_u * kUnit + kTile - 1) / kTile : 0;
     const int full = s.cost - kItemTiles;
     const float ratio = (float)tiles / (float)full;
-    const auto share = [&](int x) {
-      x -= kItemTiles;
-      return x <= 0 ? 0 : x >= full ? tiles : tiles == full ? x : min(tiles, (int)(x * ratio));
+    const auto share = [&](int y) {
+      y -= kItemTiles;
+      return y <= 0 ? 0 : y >= full ? tiles : tiles == full ? y : min(tiles, (int)(y * ratio));
     };
-    t0 = share(from);
-    t1 = share(to);
+    x.t0 = share(x.from);
+    x.t1 = share(x.to);
+    *this = x;  // every lane writes the same
+    __syncwarp();
     return true;
   }
 };
@@ -290,23 +298,25 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
 
   // The line of all items' costs, cut into one range per block; the thread whose sequences hold the
   // range's start tells the block.
-  Items<D> it;
+  static_assert(sizeof(Items<D>) == 80, "");
+  Items<D>& it = reinterpret_cast<Items<D>*>(raw_smem + C::kItems)[warp];
   {
+    Items<D> x = {};
     const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = tid * per, b1 = min(a.B, b0 + per);
     int64_t mine = 0;
     for (int i = b0; i < b1; ++i) {
-      it.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
-      mine += (int64_t)(a.hkv * it.s.blocks) * it.s.cost;
+      x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+      mine += (int64_t)(a.hkv * x.s.blocks) * x.s.cost;
     }
-    int64_t x = mine;
+    int64_t sum = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const int64_t y = __shfl_up_sync(~0u, x, d);
-      if (lane >= d) x += y;
+      const int64_t y = __shfl_up_sync(~0u, sum, d);
+      if (lane >= d) sum += y;
     }
-    if (lane == 31) ctl.sums[warp] = x;
+    if (lane == 31) ctl.sums[warp] = sum;
     __syncthreads();
-    int64_t below = x - mine, total = 0;
+    int64_t below = sum - mine, total = 0;
 #pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
       if (w < warp) below += ctl.sums[w];
@@ -316,8 +326,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     const int64_t x0 = blockIdx.x * span;
     for (int i = b0; i < b1 && below <= x0; ++i) {
       if (per > 1) {
-        it.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
-        mine = (int64_t)(a.hkv * it.s.blocks) * it.s.cost;
+        x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+        mine = (int64_t)(a.hkv * x.s.blocks) * x.s.cost;
       }
       if (x0 < below + mine) {
         ctl.start_b = i;
@@ -328,19 +338,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    it.left = min(span, total - x0);
-    it.from = it.b = it.head = it.block = 0;
-    if (it.left > 0) {
-      it.b = ctl.start_b;
-      it.s = load_seq<kRows, kTile, kItemTiles>(a, it.b, r);
+    x.left = min(span, total - x0);
+    x.from = x.b = x.head = x.block = 0;
+    if (x.left > 0) {
+      x.b = ctl.start_b;
+      x.s = load_seq<kRows, kTile, kItemTiles>(a, x.b, r);
       // which of the sequence's items, all of one cost; the estimate is off by one at most
-      int64_t item = (int64_t)((double)ctl.start_in / it.s.cost);
-      if (item * it.s.cost > ctl.start_in) --item;
-      if (ctl.start_in - item * it.s.cost >= it.s.cost) ++item;
-      it.from = (int)(ctl.start_in - item * it.s.cost);
-      it.head = (int)item / it.s.blocks;
-      it.block = (int)item - it.head * it.s.blocks;
+      int64_t item = (int64_t)((double)ctl.start_in / x.s.cost);
+      if (item * x.s.cost > ctl.start_in) --item;
+      if (ctl.start_in - item * x.s.cost >= x.s.cost) ++item;
+      x.from = (int)(ctl.start_in - item * x.s.cost);
+      x.head = (int)item / x.s.blocks;
+      x.block = (int)item - x.head * x.s.blocks;
     }
+    it = x;
   }
   const uint32_t tmem = ctl.tmem;
   const uint32_t smem32 = ptx::smem_u32(smem), packed32 = smem32 + 2 * C::kBuf;
@@ -464,34 +475,44 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ctl.q_full);
 
-        for (int j = it.t0; j < it.t1; ++j, ++tile) {
-          const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf;
+        const int tiles = it.t1 - it.t0, pos = it.base_u * kUnit + it.t0 * kTile + 64 * half, see0 = lo - pos, see1 = hi - pos;
+        for (int j = 0; j < tiles; ++j, ++tile) {
+          const uint32_t buf = tile & 1, sp = lanes + C::S + 128 * buf + 64 * half;
           all_wait(&ctl.s_full[buf], tile >> 1);
-          uint32_t sr[64];
-          ptx::tmem_ld_cols<0, 64>(sp + 64 * half, sr);
-          ptx::tmem_wait_ld();
-          const int pos0 = it.base_u * kUnit + j * kTile + 64 * half;
           // what this row sees of these columns: [c0, c1), less units that are not there
-          const int c0 = lo - pos0, c1 = hi - pos0, gone = *(volatile int*)&ctl.gone[0][tile & 7] >> (4 * half) & 15;
-          if (__any_sync(~0u, c0 > 0 || c1 < 64 || gone != 0)) {
+          const int c0 = see0 - j * kTile, c1 = see1 - j * kTile, gone = *(volatile int*)&ctl.gone[0][tile & 7] >> (4 * half) & 15;
+          const bool masked = __any_sync(~0u, c0 > 0 || c1 < 64 || gone != 0);
+          // 32 columns at a time, read twice and not kept: what the loop saves in code the instruction
+          // cache has for the other roles
+          const auto scores = [&](int c, uint32_t (&s)[32]) {
+            ptx::tmem_ld_cols<0, 32>(sp + c, s);
+            ptx::tmem_wait_ld();
+            if (masked) {
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c < c0 || c >= c1 || (gone >> (c / kUnit) & 1)) sr[c] = 0xFF800000u;
+              for (int i = 0; i < 32; ++i)
+                if (c + i < c0 || c + i >= c1 || (gone >> ((c + i) / kUnit) & 1)) s[i] = 0xFF800000u;
+            }
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            uint32_t s[32];
+            scores(c, s);
+            float top4[4] = {top, top, top, top};
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                top4[k] = fmaxf(fmaxf(top4[k], __uint_as_float(s[i + k])), __uint_as_float(s[i + 4 + k]));
+            top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
           }
-          float top4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < 64; c += 8)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              top4[i] = fmaxf(fmaxf(top4[i], __uint_as_float(sr[c + i])), __uint_as_float(sr[c + 4 + i]));
-          float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-          meet(top);  // all of S is in registers now: P may take its place
+          meet(top);
           top = fmaxf(top, theirs()) * kappa;
           if (__any_sync(~0u, top > m + 8.f)) {
             const float now = fmaxf(m, top), f = ex2(m - now);
             m = now;
             l *= f;
-            if (j > it.t0) {
+            if (j > 0) {
               // O is the softmax's once the tile before is in it; each warp takes half of the columns
               wait(&ctl, &ctl.pv_done[buf ^ 1], (tile - 1) >> 1);
               __syncwarp();
@@ -509,12 +530,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
             }
           }
           float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
+#pragma unroll 1
           for (int c = 0; c < 64; c += 32) {
-            uint32_t p[16], pl[16];
+            uint32_t s[32], p[16], pl[16];
+            scores(c, s);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float s0 = __uint_as_float(sr[c + 2 * i]), s1 = __uint_as_float(sr[c + 2 * i + 1]);
+              const float s0 = __uint_as_float(s[2 * i]), s1 = __uint_as_float(s[2 * i + 1]);
               const float x = ex2(fmaf(s0, kappa, -m)), y = ex2(fmaf(s1, kappa, -m));
               sum4[i & 3] += x + y;
               const __half2 v = __floats2half2_rn(x, y);
@@ -524,8 +546,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                 pl[i] = u32(__floats2half2_rn(x - back.x, y - back.y));
               }
             }
-            ptx::tmem_st16(sp + 32 * half + c / 2, p);
-            if (kExact) ptx::tmem_st16(sp + 64 + 32 * half + c / 2, pl);
+            // in the place of their scores: 16 columns of weights, 16 of their second parts
+            ptx::tmem_st16(sp + c, p);
+            if (kExact) ptx::tmem_st16(sp + c + 16, pl);
           }
           l += (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
           ptx::tmem_wait_st();
@@ -589,40 +612,38 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     const int ch = lane % (D / 32), row_lane = lane / (D / 32);
     uint32_t chunk = 0;
     for (bool begun = false; it.next(a, r, begun); begun = true) {
-      for (int j = it.t0; j < it.t1; ++j, ++tile) {
+      const int tiles = it.t1 - it.t0, pos0 = it.base_u * kUnit + it.t0 * kTile, first = it.first - pos0, end = it.end - pos0;
+      for (int j = 0; j < tiles; ++j, ++tile) {
         const uint32_t buf = tile & 1, base = smem32 + buf * C::kBuf;
         // keys are done with when their scores are, values when the products with the weights are
         if (tile >= 2) wait(&ctl, keys ? &ctl.s_full[buf] : &ctl.pv_done[buf], (tile - 2) >> 1);
+#pragma unroll 1
         for (int c = 0; c < C::kChunks; ++c, ++chunk) {
           const uint32_t slot = chunk % kRing;
           wait(&ctl, &ctl.ring_full[!keys][slot], chunk / kRing);
           __syncwarp();
           const uint32_t at = packed32 + (keys ? slot * C::kKeys : kRing * C::kKeys + slot * C::kValues);
-          // all reads of the stage come first: it is free again while its tokens are unpacked
           constexpr int kSteps = kChunkUnits * kUnit / (4 * kStep);
-          uint32_t w[kSteps][4], sc[kSteps][C::NG];
           const int row0 = (warp & 3) * kStep + row_lane, place = row0 % kUnit;
-#pragma unroll
+          const int gone = keys ? 0 : *(volatile int*)&ctl.gone[1][tile & 7];
+#pragma unroll 1
           for (int i = 0; i < kSteps; ++i) {
             const int unit = (4 * i * kStep + row0) / kUnit;
             const uint32_t codes_at = at + unit * (keys ? C::kCodes : C::kValue);
-            lds<16>(codes_at + place * (D / 2) + ch * 16, w[i]);
-            if (keys) lds<4 * C::NG>(at + kChunkUnits * C::kCodes + unit * C::kScales + place * 4 * C::NG, sc[i]);
-            else lds<4>(codes_at + C::kCodes + C::kScales + (place * C::NG + value_group<D>(place, ch) * 32 / G) * 4, sc[i]);
+            uint32_t w[4], sc[C::NG];
+            lds<16>(codes_at + place * (D / 2) + ch * 16, w);
+            const int row = c * kChunkUnits * kUnit + 4 * i * kStep + row0;  // of the tile
+            if (keys) {
+              lds<4 * C::NG>(at + kChunkUnits * C::kCodes + unit * C::kScales + place * 4 * C::NG, sc);
+              unpack_keys<D, G, kExact>(w, sc, base, place, ch, row & ~(kUnit - 1));
+            } else {
+              lds<4>(codes_at + C::kCodes + C::kScales + (place * C::NG + value_group<D>(place, ch) * 32 / G) * 4, sc);
+              const int pos = j * kTile + row;
+              unpack_values<D, G, kExact>(w, sc[0], base + C::kK, place, ch, row, pos >= first && pos < end && !(gone >> (row / kUnit) & 1));
+            }
           }
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&ctl.ring_empty[!keys][slot]);
-#pragma unroll
-          for (int i = 0; i < kSteps; ++i) {
-            const int row = c * kChunkUnits * kUnit + 4 * i * kStep + row0;  // of the tile
-            if (keys) {
-              unpack_keys<D, G, kExact>(w[i], sc[i], base, place, ch, row & ~(kUnit - 1));
-            } else {
-              const int pos = it.base_u * kUnit + j * kTile + row, gone = *(volatile int*)&ctl.gone[1][tile & 7];
-              unpack_values<D, G, kExact>(w[i], sc[i][0], base + C::kK, place, ch, row,
-                                          pos >= it.first && pos < it.end && !(gone >> (row / kUnit) & 1));
-            }
-          }
         }
         ptx::fence_proxy_async_smem();
         __syncwarp();
@@ -678,7 +699,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
             for (int part = 0; part < (kExact ? 2 : 1); ++part)
 #pragma unroll
               for (int ks = 0; ks < kTile / 16; ++ks)
-                ptx::umma_f16_ts(tmem + C::O, weights + 64 * part + 8 * ks, moved(values, ks * 2 * C::NA * 1024), idesc,
+                ptx::umma_f16_ts(tmem + C::O, weights + 32 * (ks >> 1) + 8 * (ks & 1) + 16 * part, moved(values, ks * 2 * C::NA * 1024), idesc,
                                  t > tile || part > 0 || ks > 0 ? 1u : 0u);
             ptx::umma_commit(&ctl.pv_done[buf]);
             ptx::umma_commit(&ctl.s_ready[buf]);
@@ -704,13 +725,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         int id_next = it.t0 < it.t1 ? entry(u_begin + lane) : -1;
         const uint8_t* src = nullptr;
         uint32_t there = 0;
-        for (int j = 0; j < (it.t1 - it.t0) * C::kChunks; ++j, ++chunk) {
+        const int chunks = (it.t1 - it.t0) * C::kChunks, head = it.head;
+        for (int j = 0; j < chunks; ++j, ++chunk) {
           const int at = (j * kChunkUnits) & 31;
           if (at == 0) {
             const int id = id_next, u = u_begin + j * kChunkUnits + lane;
             id_next = entry(u + 32);
             there = __ballot_sync(~0u, id >= 0 && id < a.n_blocks);
-            src = cache + ((((int64_t)id * a.hkv + it.head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
+            src = cache + ((((int64_t)id * a.hkv + head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
           }
           const uint32_t slot = chunk % kRing;
           if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[ring][slot], chunk / kRing - 1));
