@@ -99,8 +99,8 @@ cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_i
 cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count);
 
 // Rows of a kv head up to which the register-fed kernel is the faster one (24 sequences of 6,000 tokens, 4
-// kv heads, d = 128, 1 to n drafted tokens: 24 rows 52 us against 90, 64 rows 81 against 95, 96 rows 106
-// against 98; d = 64: 33 against 60, 49 against 61, 63 against 62).
+// kv heads, 1 to n drafted tokens, d = 128: 24 rows 46 us against 69, 48 rows 61 against 69, 64 rows 75
+// against 70; d = 64: 31 against 57, 38 against 58, 47 against 58).
 constexpr int64_t kFewRows = 64;
 
 }  // namespace kv4

