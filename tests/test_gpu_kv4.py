@@ -360,6 +360,19 @@ def test_another_stream_with_no_wait_for_the_default_one():
     assert all(torch.equal(o, want) for o in outs)
 
 
+@pytest.mark.parametrize("B,max_q", [(8192, 1), (2100, 3), (1500, 9)])
+def test_more_sequences_than_a_block_has_threads(B, max_q):
+    rng = np.random.default_rng(B)
+    qlens = None if max_q == 1 else rng.integers(0, max_q + 1, B).tolist()
+    lens = np.where(rng.random(B) < 0.7, 0, rng.integers(0, 40, B))
+    lens[[5, B - 1]] = 900, 300
+    if qlens is not None:
+        qlens[0] = max_q
+        lens = np.maximum(lens, qlens) * (rng.random(B) < 0.9)  # a few whose tokens are not there: rows of 0
+    c = Cache(rng, lens.tolist(), 1, 64, 64, 32)
+    _attend(c, _q(rng, B if qlens is None else sum(qlens), 8, 64, torch.bfloat16), qlens)
+
+
 @pytest.mark.parametrize("qlens", [None, [3, 1, 0, 4, 2], [11, 4, 0, 1, 2]])
 def test_a_workspace_of_any_content_serves_call_after_call_and_graphs_in_turn(qlens):
     rng = np.random.default_rng(18)
