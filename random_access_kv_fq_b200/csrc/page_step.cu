@@ -10,7 +10,8 @@
 // order (1) all reads of lens and free_count before they may be overwritten in place and (2)
 // released pages before they are handed out again.  A warp writes 32 or 256 slots at a time: it finds
 // the requests of the first and the last by bisection and its lanes search only between them.
-// Measured: 256 decodes 5.0 us; 2,048 requests with prompts, releases and 262,144 slots 21 us.
+// Measured: 256 decodes 5.0 us; 2,048 requests with prompts, releases and 262,144 slots 15 us.
+#include <atomic>
 #include <climits>
 
 #include <cooperative_groups.h>
@@ -23,7 +24,6 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kCluster = 8;
 
 __device__ __forceinline__ int sat(int64_t x) { return x > INT_MAX ? INT_MAX : (int)x; }
 
@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
     if (ALONE) __syncthreads(); else cluster.sync();
   };
   const int rank = ALONE ? 0 : (int)cluster.block_rank();
-  const int threads = blockDim.x, n_thr = threads * (ALONE ? 1 : kCluster), me = rank * threads + threadIdx.x;
+  const int threads = blockDim.x, n_thr = threads * (ALONE ? 1 : (int)cluster.num_blocks()), me = rank * threads + threadIdx.x;
   const int per = (a.B + threads - 1) / threads;
   const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
   const int64_t room = (int64_t)a.max_blocks << page_shift;
@@ -232,33 +232,62 @@ __global__ void __launch_bounds__(1024) page_step_kernel(PageArgs a, int page_sh
   }
 }
 
+// Blocks of the cluster that a large step runs on: 16, or the 8 that are always to be had where the device
+// cannot place 16 (2,048 requests, prompts, releases and 262,144 slots: 14.8 us with 16, 21.0 with 8).
+cudaError_t cluster_blocks(cudaLaunchConfig_t& cfg, int* blocks) {
+  static std::atomic<int> known[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  *blocks = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (*blocks > 0) return cudaSuccess;
+  e = cudaFuncSetAttribute(page_step_kernel<false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e != cudaSuccess) return e;
+  // asked for the largest step, so that the answer holds for every one
+  cudaLaunchConfig_t most = cfg;
+  most.blockDim = dim3(1024);
+  most.dynamicSmemBytes = sizeof(int) * (4 * (size_t)kMaxRequests + 1);
+  e = cudaFuncSetAttribute(page_step_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most.dynamicSmemBytes);
+  if (e != cudaSuccess) return e;
+  int fit = 0;
+  most.gridDim = dim3(16);
+  most.attrs[0].val.clusterDim.x = 16;
+  e = cudaOccupancyMaxActiveClusters(&fit, page_step_kernel<false>, &most);
+  if (e != cudaSuccess) cudaGetLastError();  // not a size that it knows
+  *blocks = e == cudaSuccess && fit > 0 ? 16 : 8;
+  if (dev < 64) known[dev].store(*blocks, std::memory_order_relaxed);
+  return cudaSuccess;
+}
+
 }  // namespace
 
 cudaError_t launch_page_step(const PageArgs& a, cudaStream_t st) {
   const size_t smem = sizeof(int) * (4 * (size_t)a.B + 1);
   // One block does a small step: its barriers cost less.  A cluster shares the searches and stores of a
   // large one.  In us, one block and the cluster: 256 decodes 5.0 and 6.8, with every 17th request
-  // released 8.6 and 8.0; 1,024 such requests 14.1 and 11.1; 4,096 of them 36.2 and 16.7.
+  // released 8.4 and 8.0; 1,024 such requests 14.1 and 10.9; 4,096 of them 36.2 and 15.7.
   // Few requests need few warps: their sums are sooner there.
   const bool alone = (int64_t)a.n_slots + a.B <= 1024;
   const auto kernel = alone ? page_step_kernel<true> : page_step_kernel<false>;
-  if (smem > 48 * 1024 - sizeof(Two) * 32) {  // what a block may have unasked
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
   int shift = 0;
   while ((1 << shift) < a.page) ++shift;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(alone ? 1 : kCluster);
+  cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(a.B <= 256 && a.n_slots <= 2048 ? 256 : 1024);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kCluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  at[0].val.clusterDim.x = at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = alone ? 0 : 1;
+  if (!alone) {
+    int blocks = 8;
+    const cudaError_t e = cluster_blocks(cfg, &blocks);
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(blocks);
+    at[0].val.clusterDim.x = blocks;
+  }
   const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a, shift);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
