@@ -18,11 +18,12 @@
 // score passes it by 8; moving it rescales O in tensor memory.
 //
 // A product of 128 x 128 x 16 takes 64 cycles (of 128 x 64 x 16: 50 to 57, so tiles are 128 tokens), so
-// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  It takes about 3,900
-// and 4,500 (3 chunks of 1,024 queries over up to 8K tokens, 32 query and 8 kv heads: 212 and 293 us, 620
-// and 448 TFLOP/s): 9,000 warp instructions of unpacking and softmax a tile, and roles whose code together
-// does not stay in the instruction caches (a seventh of the stalls), hold the tensor pipe at 41 %.
-// Measured and not kept: 8 unpacking warps more (fp16 310 us), 16 softmax warps, softmax groups on
+// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  It takes about 3,700
+// and 4,000 (3 chunks of up to 1,024 queries over up to 8K tokens, 32 query and 8 kv heads: 218 and 247 us,
+// 600 and 530 TFLOP/s): 9,000 warp instructions of unpacking and softmax a tile (fp16), and roles whose code
+// together does not stay in the instruction caches (a seventh of the stalls).  A change of item takes 10,000
+// to 15,000 cycles, so ranges are cut by tokens and parts of one tile are not made.
+// Measured and not kept: 8 unpacking warps more, 16 softmax warps, softmax groups on
 // alternate tiles, asynchronous copies by the unpacking warps.
 #include <atomic>
 #include <cfloat>
@@ -57,7 +58,7 @@ __device__ unsigned int g_kv4_rows_wait_timeouts = 0;  // blocks whose bounded w
 constexpr int kRows = 128;      // rows of a block's item
 constexpr int kTile = 128;      // tokens of a tile
 constexpr int kTileUnits = kTile / kUnit;
-constexpr int kItemTiles = 2;   // an item's fixed cost, in tiles
+constexpr int kItemTiles = 6;   // an item's fixed cost, in tiles: its queries, its end, the first tile's way
 constexpr int kSoftmaxWarps = 8;  // warps w and w + 4 share 32 rows, 64 columns each
 constexpr int kKeyWarps = 4, kValueWarps = 4, kUnpackWarps = kKeyWarps + kValueWarps;
 constexpr int kWarps = kSoftmaxWarps + kUnpackWarps + 4;  // two for the products, two loaders
@@ -85,7 +86,7 @@ struct Shape {
   static constexpr int kRing = D == 64 ? 8 : EXACT ? 2 : 4;  // what shared memory leaves
   static constexpr size_t kControl = 1024;
   static constexpr size_t kItems = kControl + 2 * kBuf + kRing * (kKeys + kValues);
-  static constexpr size_t kSmem = kItems + kWarps * 80;
+  static constexpr size_t kSmem = kItems + kWarps * 96;
   // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
   static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
@@ -122,49 +123,91 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
 }
 enum { kBarSoftmax = 1, kBarPair = 2 };
 
+// A sequence's place on the line.  Row block i (from 1) of a head sees 128 / r tokens more than the one
+// before, none while its rows lie before the first token, and no more than the window: in steps of
+// 128 / r tokens clamp(base + i, 0, top).  Its cost is that and a fixed part; the sums are closed forms, so
+// that ranges are equal in tokens though later rows of a prompt see more (a prompt of 2,048 tokens: the
+// fullest block has 34 tiles where the mean is 30; with one cost for all row blocks of a sequence 56).
+struct Line {
+  int64_t base, top;
+  int fixed;
+  __device__ __forceinline__ Line(const AttnArgs& a, const Seq& s, int r)
+      : base(((int64_t)(s.n - s.m + 1) * r) >> 7),
+        top(a.window > 0 ? (((int64_t)min(a.window, 1 << 30) * r) >> 7) + 2 : (int64_t)1 << 40), fixed(kItemTiles * r) {}
+  __device__ __forceinline__ int64_t cost(int block) const {
+    return fixed + min(max(base + block + 1, (int64_t)0), top);
+  }
+  // of a head's first k row blocks
+  __device__ __forceinline__ int64_t sum(int k) const { return ramp(base, k) - ramp(base - top, k) + (int64_t)k * fixed; }
+
+ private:
+  // max(0, b + 1) + .. + max(0, b + k)
+  static __device__ __forceinline__ int64_t ramp(int64_t b, int64_t k) {
+    const int64_t i = max((int64_t)1, 1 - b), n = max((int64_t)0, k - i + 1);
+    return n * b + (i + k) * n / 2;
+  }
+};
+
 // The items of a block's range of the line, one at a time, the same in every role.  Each warp has its own
 // in shared memory: in registers they would be spilled.
 template <int D>
 struct Items {
-  int64_t left;
-  int from, b, head, block;
+  int64_t left, from;
+  int b, head, block;  // block: its row block
   Seq s;
   // of the current item
-  int to, rb, end, first, base_u, t0, t1, past;
+  int end, first, base_u, t0, t1, past;
+  int64_t to, cost;
   __device__ __forceinline__ bool next(const AttnArgs& a, int r, bool begun) {
     __syncwarp();
     Items x = *this;
     __syncwarp();
-    if (begun) {
-      x.from = 0;
-      if (x.left > 0 && ++x.block == x.s.blocks) {
-        x.block = 0;
-        if (++x.head == a.hkv) {
-          x.head = 0;
-          do x.s = load_seq<kRows, kTile, kItemTiles>(a, ++x.b, r); while (x.s.blocks == 0);
+    for (;; begun = true) {
+      if (begun) {
+        x.from = 0;
+        if (x.left > 0 && ++x.block == x.s.blocks) {
+          x.block = 0;
+          if (++x.head == a.hkv) {
+            x.head = 0;
+            do x.s = load_seq<kRows, kTile, kItemTiles>(a, ++x.b, r); while (x.s.blocks == 0);
+          }
         }
       }
+      if (x.left <= 0) return false;
+      const Seq& s = x.s;
+      const Line line(a, s, r);
+      x.cost = line.cost(x.block);
+      x.to = min(x.cost, x.from + x.left);
+      x.left -= x.to - x.from;
+      x.past = s.n - s.m + 1;
+      const uint32_t row0 = x.block * kRows, row1 = min(x.block * kRows + kRows, s.rows) - 1;
+      x.end = max(0, x.past + (int)(row1 / (uint32_t)r));
+      x.first = a.window > 0 ? max(0, x.past + (int)(row0 / (uint32_t)r) - a.window) : 0;
+      x.base_u = x.first / kUnit;
+      const int tiles = x.end > x.first ? (x.end - x.base_u * kUnit + kTile - 1) / kTile : 0;
+      const int64_t full = x.cost - line.fixed;
+      const float ratio = (float)tiles / (float)full;
+      // Tiles before a place of the item.  No part has fewer than two: it would cost more than it takes over.
+      // A place so near an end counts as that end, to the blocks on both sides of it.
+      const auto share = [&](int64_t y) {
+        if (y <= 0) return 0;
+        if (y >= x.cost) return tiles;
+        y -= line.fixed;
+        const int n = y >= full ? tiles : y <= 0 ? 0 : min(tiles, (int)(y * ratio));
+        return n > tiles - 2 ? tiles : n < 2 ? 0 : n;
+      };
+      x.t0 = share(x.from);
+      x.t1 = share(x.to);
+      if (x.from > 0) {
+        if (x.t0 == tiles) continue;  // the block before ends it
+        if (x.t0 == 0) x.from = 0;
+      }
+      if (x.to < x.cost) {
+        if (x.t1 == tiles) x.to = x.cost;
+        else if (x.t1 == 0) return false;  // the block behind begins it
+      }
+      break;
     }
-    if (x.left <= 0) return false;
-    const Seq& s = x.s;
-    x.to = (int)min((int64_t)s.cost, x.from + x.left);
-    x.left -= x.to - x.from;
-    // row blocks from both ends in turn: two neighbours see about as many tokens as any two
-    x.rb = x.block & 1 ? s.blocks - 1 - (x.block >> 1) : x.block >> 1;
-    x.past = s.n - s.m + 1;
-    const uint32_t row0 = x.rb * kRows, row1 = min(x.rb * kRows + kRows, s.rows) - 1;
-    x.end = max(0, x.past + (int)(row1 / (uint32_t)r));
-    x.first = a.window > 0 ? max(0, x.past + (int)(row0 / (uint32_t)r) - a.window) : 0;
-    x.base_u = x.first / kUnit;
-    const int tiles = x.end > x.first ? (x.end - x.base_u * kUnit + kTile - 1) / kTile : 0;
-    const int full = s.cost - kItemTiles;
-    const float ratio = (float)tiles / (float)full;
-    const auto share = [&](int y) {
-      y -= kItemTiles;
-      return y <= 0 ? 0 : y >= full ? tiles : tiles == full ? y : min(tiles, (int)(y * ratio));
-    };
-    x.t0 = share(x.from);
-    x.t1 = share(x.to);
     *this = x;  // every lane writes the same
     __syncwarp();
     return true;
@@ -304,7 +347,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
 
   // The line of all items' costs, cut into one range per block; the thread whose sequences hold the
   // range's start tells the block.
-  static_assert(sizeof(Items<D>) == 80, "");
+  static_assert(sizeof(Items<D>) == 96, "");
   Items<D>& it = reinterpret_cast<Items<D>*>(raw_smem + C::kItems)[warp];
   {
     Items<D> x = {};
@@ -312,7 +355,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     int64_t mine = 0;
     for (int i = b0; i < b1; ++i) {
       x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
-      mine += (int64_t)(a.hkv * x.s.blocks) * x.s.cost;
+      mine += a.hkv * Line(a, x.s, r).sum(x.s.blocks);
     }
     int64_t sum = mine;
 #pragma unroll
@@ -328,12 +371,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       if (w < warp) below += ctl.sums[w];
       total += ctl.sums[w];
     }
-    const int64_t span = max((int64_t)(total * (1.0 / kCtas)) + 1, (int64_t)kItemTiles + 2);
+    const int64_t span = max((int64_t)(total * (1.0 / kCtas)) + 1, (int64_t)(kItemTiles + 1) * r);
     const int64_t x0 = blockIdx.x * span;
     for (int i = b0; i < b1 && below <= x0; ++i) {
       if (per > 1) {
         x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
-        mine = (int64_t)(a.hkv * x.s.blocks) * x.s.cost;
+        mine = a.hkv * Line(a, x.s, r).sum(x.s.blocks);
       }
       if (x0 < below + mine) {
         ctl.start_b = i;
@@ -349,13 +392,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     if (x.left > 0) {
       x.b = ctl.start_b;
       x.s = load_seq<kRows, kTile, kItemTiles>(a, x.b, r);
-      // which of the sequence's items, all of one cost; the estimate is off by one at most
-      int64_t item = (int64_t)((double)ctl.start_in / x.s.cost);
-      if (item * x.s.cost > ctl.start_in) --item;
-      if (ctl.start_in - item * x.s.cost >= x.s.cost) ++item;
-      x.from = (int)(ctl.start_in - item * x.s.cost);
-      x.head = (int)item / x.s.blocks;
-      x.block = (int)item - x.head * x.s.blocks;
+      const Line line(a, x.s, r);
+      const int64_t head = line.sum(x.s.blocks);
+      x.head = (int)(ctl.start_in / head);
+      x.from = ctl.start_in - x.head * head;
+      // the last row block that begins at or before the place
+      int lo = 0, hi = x.s.blocks;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (line.sum(mid) <= x.from) lo = mid; else hi = mid;
+      }
+      x.block = lo;
+      x.from -= line.sum(lo);
     }
     it = x;
   }
@@ -388,11 +436,11 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       ptx::tc_fence_after();
     };
     for (bool begun = false; it.next(a, r, begun); begun = true) {
-      const uint32_t row = it.rb * kRows + my_row;
+      const uint32_t row = it.block * kRows + my_row;
       const bool in = row < (uint32_t)it.s.rows;
       const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
       float m = -FLT_MAX, l = 0.f, kappa = 0.f;
-      const uint32_t last_row = min(it.rb * kRows + kRows, it.s.rows) - 1;
+      const uint32_t last_row = min(it.block * kRows + kRows, it.s.rows) - 1;
       const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? hi - a.window : 0;
       if (it.t0 < it.t1) {
         // this thread's half row of q, by a power of two in fp16, its keys' order of coordinates
@@ -567,7 +615,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
         l += theirs();
         ptx::tc_fence_after();
       }
-      const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.s.cost;
+      const bool any = it.t0 < it.t1, whole = it.from == 0 && it.to == it.cost;
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const int k = it.from > 0 ? 0 : 1;
       RowsPart<D>* part = out_part + blockIdx.x * 2 + k;
@@ -602,7 +650,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           part->l[my_row] = l;
         }
         left_part[k] = 1;
-        if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{it.to == it.s.cost ? 3 : 1, it.s.q0, it.s.rows, it.head, it.rb};
+        if (tid == 0) out_hdr[blockIdx.x * 2 + k] = PartHeader{it.to == it.cost ? 3 : 1, it.s.q0, it.s.rows, it.head, it.block};
       }
       // O is read before the next item's first product: its q comes after the warps met here
       if (any) meet(0.f);
