@@ -99,8 +99,8 @@ cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_i
 cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count);
 
 // Rows of a kv head up to which the register-fed kernel is the faster one (24 sequences of 6,000 tokens, 4
-// kv heads, 1 to n drafted tokens, d = 128: 24 rows 46 us against 70, 48 rows 61 against 72, 64 rows 75
-// against 74; d = 64: 31 against 62, 38 against 64, 47 against 65).
+// kv heads, 1 to n drafted tokens, d = 128: 32 rows 49 us against 74, 48 rows 61 against 74, 64 rows 75
+// against 74; d = 64: 33 against 66, 38 against 66, 47 against 66).
 constexpr int64_t kFewRows = 64;
 
 }  // namespace kv4
