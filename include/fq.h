@@ -388,8 +388,10 @@ fq_status fq_page_step(const int32_t* lens, const int32_t* new_lens, int B, int3
  *   k_values, v_values  [n, Hkv, d] of `type`, 16-byte aligned, or NULL: what the codes stand for,
  *             c s + z rounded to `type`, for every token (for a prefill that attends to its own
  *             tokens as later steps will see them).
+ *   Groups that span 65504 or more are written, but fq_kv4_attn does not take them.
  * In fp32, per group: z = fp16(min), s = fp16((max - z) * fp32(1/15)) (both within +-65504),
- * c = clamp(rint((x - z) * (1 / s)), 0, 15), c = 0 where s = 0.
+ * c = clamp(rint((x - z) * (1 / s)), 0, 15), c = 0 where s = 0.  A group that holds a NaN has z and s
+ * NaN and codes of 0: all of it stands for NaN, other groups are as they would be without it.
  */
 fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, int Hkv, int d,
                        int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
@@ -412,15 +414,16 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  *             query tokens (its last ones) included.  Query token i of m sees the tokens below
  *             e = kv_len - m + i + 1 and, with window > 0, not below e - window.
  *   block_tables  [B, max_blocks] int32: a sequence's pages in order.  Tokens on a page outside
- *             [0, n_blocks) are not seen.  Nothing that is not seen is read into the result: it
- *             may hold anything.
+ *             [0, n_blocks) are not seen.  What no query token of a sequence sees may hold
+ *             anything.
  *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
  *             sequence has are left as they were.
  *   workspace fq_kv4_attn_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0), owned by the
  *             caller, of any content, and overwritten; calls that may overlap (two streams, two captured
  *             graphs) need one each.
  * Precondition: the groups of tokens that are seen span less than 65504 (15 s and c s + z are fp16
- * numbers on the way).
+ * numbers on the way).  A NaN in a key makes the rows that see it NaN; a NaN in a value those and,
+ * as 0 times NaN, it may be other query tokens' rows of the sequence.
  * B <= 8192, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.
  */
 fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,

@@ -4,6 +4,7 @@
 //   z = fp16(min),  s = fp16((max - z) * fp32(1/15)),  c = clamp(rint((x - z) * (1 / s)), 0, 15)
 // (c = 0 where s = 0); the cache then stands for c s + z.  The record keeps z and s in 16 bits, so
 // the codes are taken against the rounded z and s: what is lost to their rounding is not lost twice.
+// A NaN makes its group's min, max, z and s NaN: the group reads as NaN and its codes are 0.
 //
 // Bound by HBM: 2 d elements in, d + 8 d / G bytes out (and 2 d elements with the values) per (token,
 // kv head).  One thread takes 8 coordinates (a 16-byte load and one 32-bit word of codes) of a
@@ -61,21 +62,43 @@ __device__ __forceinline__ uint32_t pack2(__nv_bfloat16, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The least and the largest of three, NaN if one of them is (fminf and fmaxf leave a NaN out); one instruction.
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// The same of two.
+__device__ __forceinline__ float min2(float a, float b) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+__device__ __forceinline__ float max2(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // Quantises this thread's 8 coordinates with the other lanes of its group; returns the code word
 // and, in `sz`, the group's s (low half) and z.
 template <typename T, int G>
 __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, T* values) {
-  // three at a time: one instruction each
-  float lo = fminf(fminf(fminf(fminf(x[0], x[1]), x[2]), fminf(fminf(x[3], x[4]), x[5])), fminf(x[6], x[7]));
-  float hi = fmaxf(fmaxf(fmaxf(fmaxf(x[0], x[1]), x[2]), fmaxf(fmaxf(x[3], x[4]), x[5])), fmaxf(x[6], x[7]));
+  float lo = min3(min3(x[0], x[1], x[2]), min3(x[3], x[4], x[5]), min2(x[6], x[7]));
+  float hi = max3(max3(x[0], x[1], x[2]), max3(x[3], x[4], x[5]), max2(x[6], x[7]));
 #pragma unroll
   for (int m = 1; m < G / 8; m <<= 1) {
-    lo = fminf(lo, __shfl_xor_sync(~0u, lo, m));
-    hi = fmaxf(hi, __shfl_xor_sync(~0u, hi, m));
+    lo = min2(lo, __shfl_xor_sync(~0u, lo, m));
+    hi = max2(hi, __shfl_xor_sync(~0u, hi, m));
   }
-  const __half z16 = __float2half_rn(fminf(fmaxf(lo, -65504.f), 65504.f));
+  const __half z16 = __float2half_rn(min2(max2(lo, -65504.f), 65504.f));
   const float z = __half2float(z16);
-  const __half s16 = __float2half_rn(fminf(fmaxf((hi - z) * (1.0f / 15.0f), 0.f), 65504.f));
+  const __half s16 = __float2half_rn(min2(max2((hi - z) * (1.0f / 15.0f), 0.f), 65504.f));
   const float s = __half2float(s16);
   const float inv = s > 0.f ? 1.0f / s : 0.f;
   sz = (uint32_t)__half_as_ushort(s16) | ((uint32_t)__half_as_ushort(z16) << 16);
@@ -83,7 +106,8 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sz, 
   float c[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) c[i] = __fmul_rn(__fsub_rn(x[i], z), inv);
-  // the roundings of z and s seldom move a group's ends past half a step
+  // The roundings of z and s seldom move a group's ends past half a step.  In a group with a NaN all of c is
+  // NaN, the test fails, and the clamping, which leaves a NaN out, makes it 0.
   if (!((lo - z) * inv >= -0.5f && (hi - z) * inv < 15.5f)) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) c[i] = fminf(fmaxf(c[i], 0.f), 15.f);

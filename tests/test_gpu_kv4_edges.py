@@ -1,0 +1,64 @@
+"""The 4-bit paged cache on the GPU where its inputs are at their limits: values that are not numbers,
+weights far below the largest, counts and windows outside what a batch holds.  Bounds as in test_gpu_kv4."""
+import numpy as np
+import pytest
+import torch
+
+import random_access_kv_fq_b200 as fq
+from tests import kv4_ref as ref
+from tests.test_gpu_kv4 import SHAPES, Cache, _check_attn, _cpu, _dev, _q
+
+pytestmark = pytest.mark.gpu
+
+
+def _scale_bytes(d, group):
+    """First bytes of every step and zero of a unit."""
+    return sorted(b for at in (ref.key_scale_at, ref.value_scale_at) for t in range(16) for g in range(d // group)
+                  for b in at(t, g, d, group))
+
+
+# ------------------------------------------------------------------ write
+
+@pytest.mark.parametrize("d,group", SHAPES)
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_a_nan_makes_its_group_nan_and_leaves_the_others_alone(d, group, dtype):
+    rng = np.random.default_rng(d + group)
+    n, hkv = 12, 2
+    x = rng.standard_normal((2, n, hkv, d)).astype(np.float32)
+    x[0, 1, 0, 3] = x[0, 2, 1, d - 1] = x[1, 3, 0, group - 1] = np.nan   # one coordinate
+    x[0, 4], x[1, 4, 1, :group] = np.nan, np.nan                           # whole groups
+    x[0, 5, 0, 9], x[1, 6, 1, 2], x[0, 7, 1] = np.inf, -np.inf, -np.inf
+    x[1, 8, 0, :2] = np.inf, np.nan
+    k, v = (torch.from_numpy(a).to(dtype) for a in x)
+    cache = rng.integers(0, 256, (1, hkv, 1, ref.unit_bytes(d, group)), dtype=np.uint8)
+    slots = rng.permutation(16)[:n].astype(np.int32)
+    got = _dev(cache)
+    values = fq.fq_kv4_write(k.cuda(), v.cuda(), _dev(slots), got, group, values=True)
+    got = _cpu(got)
+    with np.errstate(invalid="ignore"):
+        ref.write(cache, k.float().numpy(), v.float().numpy(), slots, group)
+    at = _scale_bytes(d, group)
+    codes = np.setdiff1d(np.arange(cache.shape[-1]), np.concatenate([at, np.array(at) + 1]))
+    np.testing.assert_array_equal(got[..., codes], cache[..., codes])
+    halves = lambda c: np.ascontiguousarray(c[..., 16 * d:]).view(np.float16)  # noqa: E731
+    np.testing.assert_array_equal(halves(got), halves(cache))                  # a NaN equals a NaN
+    for a, b in zip((k, v), values):
+        with np.errstate(invalid="ignore", over="ignore"):
+            want = torch.from_numpy(ref.values(*ref.quantise(a.float().numpy(), group), group).astype(np.float32)).to(dtype)
+        torch.testing.assert_close(b.cpu(), want, rtol=0, atol=0, equal_nan=True)
+
+
+@pytest.mark.parametrize("hq", [4, 66])  # rows of a kv head: few, and more than 64
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_a_key_that_is_not_a_number_reaches_only_the_rows_that_see_it(hq, dtype):
+    rng = np.random.default_rng(hq)
+    c = Cache(rng, [35, 20], 1, 64, 32, 16)
+    want, A, S = ref.attend(_cpu(_q(np.random.default_rng(1), 4, hq, 64, dtype).double()), c.host, c.tables, c.lens, 32, [0, 2, 4])
+    q, pool = _q(np.random.default_rng(1), 4, hq, 64, dtype), _dev(c.host)
+    key = torch.full((1, 1, 64), float("nan"), dtype=dtype, device="cuda")
+    slot = int(c.tables[0, 34 // 16]) * 16 + 34 % 16  # the last token of sequence 0: its first query token does not see it
+    fq.fq_kv4_write(key, torch.ones_like(key), _dev(np.array([slot], dtype=np.int32)), pool, 32)
+    out = fq.fq_kv4_attn(q, pool, _dev(c.tables), _dev(c.lens), 32, cu_q=_dev(np.array([0, 2, 4], dtype=np.int32)), max_q=2)
+    assert torch.isnan(out[1]).all()
+    for i in (0, 2, 3):
+        _check_attn(out[i], want[i], A[i], S[i], 64, dtype, rows=2 * hq)
