@@ -417,7 +417,8 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  *             [0, n_blocks) are not seen.  What no query token of a sequence sees may hold
  *             anything.
  *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
- *             sequence has are left as they were.
+ *             sequence has are left as they were.  A token whose weight is below 2^-32
+ *             of the row's largest may count as 0.
  *   workspace fq_kv4_attn_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0), owned by the
  *             caller, of any content, and overwritten; calls that may overlap (two streams, two captured
  *             graphs) need one each.

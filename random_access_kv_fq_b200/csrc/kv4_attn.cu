@@ -12,7 +12,7 @@
 //            Steps multiply in fp32 after the products, zeros enter as one more product with the
 //            groups' sums of q (in two fp16 parts), so scores carry no 16-bit rounding: q itself
 //            is scaled to fp16 by a power of two per row.
-//   softmax  base 2, against a running maximum that moves only when a score passes it by 8.
+//   softmax  base 2, against a running maximum that moves only when a score passes it by 8 (kLow, kLag).
 //   values   O^T += V^T P^T with V = fp16(c s + z) and P in fp16, for fp16 outputs in two parts:
 //            one rounding of 2^-12 then, beside the output's own; bf16's own is 2^-9.
 // A warp's unfinished ranges are joined in shared memory, a block's by the last block to leave a part
@@ -110,7 +110,7 @@ struct Warp {
   uint32_t qz[NT][2];        // sums of q over the groups, two parts (the second word for NG = 8 only)
   float kappa[NT][2];        // score scale of rows 2 t, 2 t + 1 of the tile
   int hi[NT][2], lo[NT][2];  // tokens that the rows see: [lo, hi)
-  float o[NT][MT][4], m[NT][2], l[NT][2];
+  float o[NT][MT][4], m[NT][2], l[NT][2];  // m: kLow below the scores' maximum
 
   __device__ __forceinline__ void reset() {
 #pragma unroll
@@ -301,7 +301,7 @@ struct Warp {
         high = fmaxf(high, y[nt][i]);
       }
     }
-    if (__any_sync(~0u, high > 8.f)) {
+    if (__any_sync(~0u, high > kLow + kLag)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -311,7 +311,7 @@ struct Warp {
           float top = fmaxf(xa, xb);
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, d));
-          top = fmaxf(top, m[nt][c]);
+          top = fmaxf(top - kLow, m[nt][c]);
           const float f = ex2(m[nt][c] - top);
           y[nt][c] = xa - top;
           y[nt][c + 2] = xb - top;

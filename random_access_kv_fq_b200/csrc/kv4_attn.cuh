@@ -13,6 +13,12 @@ namespace kv4 {
 
 constexpr int kCtas = 148;  // one block per SM
 
+// Weights are fp16 numbers in the products, whose range ends at 2^16 and at 2^-25.  They are taken against a
+// number kLow below the row's maximum, which moves when a score passes that maximum by kLag: the largest weights
+// are 2^7, never above 2^15, and one of 2^-32 of the largest still counts.  Against the maximum itself those
+// below 2^-25 were lost; 131,072 such tokens together weigh up to 1/256 of the largest.
+constexpr float kLow = 7.f, kLag = 8.f;
+
 struct Seq {
   int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
   int cost;                    // of each of its row blocks: the most that one may see

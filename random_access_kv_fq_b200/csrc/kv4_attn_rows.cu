@@ -15,7 +15,7 @@
 //   S = Q (s_hi C)^T + Q (s_lo C)^T + qsum Z^T,
 // the last one a 16-wide product of the groups' sums of q (in two parts) with the zeros; weights are in
 // two parts, O = P_hi V + P_lo V.  The softmax runs to base 2 against a maximum that moves only when a
-// score passes it by 8; moving it rescales O in tensor memory.
+// score passes it by 8 (kLow, kLag); moving it rescales O in tensor memory.
 //
 // A product of 128 x 128 x 16 takes 64 cycles (of 128 x 64 x 16: 50 to 57, so tiles are 128 tokens), so
 // a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  It takes about 3,700
@@ -562,8 +562,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           }
           meet(top);
           top = fmaxf(top, theirs()) * kappa;
-          if (__any_sync(~0u, top > m + 8.f)) {
-            const float now = fmaxf(m, top), f = ex2(m - now);
+          if (__any_sync(~0u, top > m + (kLow + kLag))) {
+            const float now = fmaxf(m, top - kLow), f = ex2(m - now);
             m = now;
             l *= f;
             if (j > 0) {

@@ -62,3 +62,36 @@ def test_a_key_that_is_not_a_number_reaches_only_the_rows_that_see_it(hq, dtype)
     assert torch.isnan(out[1]).all()
     for i in (0, 2, 3):
         _check_attn(out[i], want[i], A[i], S[i], 64, dtype, rows=2 * hq)
+
+
+# ------------------------------------------------------------------ attention
+
+@pytest.mark.parametrize("B,hq,hkv", [(296, 8, 8), (148, 66, 1)])  # a warp, and a block of the other kernel, to an item
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_many_small_weights_beside_a_large_one_are_not_lost(B, hq, hkv, dtype):
+    """One token of weight 1 and 131,071 of 2^-25.5: together they move the result by 2^-8.5.  Weights are
+    fp16 numbers of at least 2^7 for the largest: each is off by at most 2^-25 or 2^-32 of the largest.  Sums
+    of weights and of weighted values take n / 16 additions of 2^-24 each."""
+    d, group, page, n = 64, 64, 64, 1 << 17
+    k, v = np.zeros((2, 2 * page, hkv, d), dtype=np.float32)
+    v[:] = np.linspace(0.5, 1.5, d)
+    k[page + 5, :, 0] = 25.5 * np.log(2)  # the large one, of value 0, in page 1; every token of page 0 is alike
+    v[page + 5] = 0
+    host = np.zeros((2, hkv, page // 16, ref.unit_bytes(d, group)), dtype=np.uint8)
+    ref.write(host, k, v, np.arange(2 * page), group)
+    kq, vq = ref.read(host, np.array([0, page + 5]), d, group)
+    tables = np.zeros((B, n // page), dtype=np.int32)
+    tables[np.arange(B), np.linspace(0, n // page - 1, B).astype(int)] = 1  # anywhere in the context
+    q = np.zeros((B, hq, d))
+    q[..., 0] = 1
+    out = fq.fq_kv4_attn(torch.from_numpy(q).to(dtype).cuda(), _dev(host), _dev(tables), _dev(np.full(B, n, dtype=np.int32)),
+                         group, scale=1.0)
+    p = (n - 1) * np.exp(kq[0, 0, 0] - kq[1, 0, 0])
+    A = p / (1 + p) * vq[0, 0]
+    lost = n * 2.0 ** -32 * np.abs(vq[0, 0])
+    want = np.broadcast_to(A, out.shape)
+    S = kq[1, 0, 0]
+    got = _cpu(out.double())
+    rel = 2.0 ** -10 + 2 * n / 16 * 2.0 ** -24 + 2.0 ** -14 + (2 * (d + 8) * 2.0 ** -23 + (2.0 ** -10 if dtype == torch.bfloat16 and hq > 64 else 0)) * S
+    half_eps = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
+    assert (np.abs(got - want) <= (half_eps + rel) * want + lost + 2.0 ** -24).all(), (got[0, 0, :4], want[0, 0, :4])
