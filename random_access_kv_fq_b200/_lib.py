@@ -560,14 +560,19 @@ def fq_kv4_write(k, v, slots, cache, group: int, values: bool = False, stream=No
     return (kv, vv) if values else None
 
 
-def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: int = 1,
+def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: Optional[int] = None,
                 window: int = 0, scale: Optional[float] = None, out=None, workspace=None,
                 stream=None):
     """Causal attention of q [n_q, Hq, d] (fp16 or bf16, last axis contiguous) over the 4-bit cache
     [n_blocks, Hkv, page / 16, unit bytes] through block_tables [B, max_blocks] and kv_lens [B]
-    (int32).  cu_q [B + 1] (int32) gives the sequences' rows of q, at most max_q each; without it
-    every sequence has one.  window > 0: only the last `window` tokens are seen.  Returns out
-    [n_q, Hq, d] of q's type."""
+    (int32).  cu_q [B + 1] (int32) gives the sequences' rows of q, at most max_q each, which has to be
+    given then; without it every sequence has one.  window > 0: only the last `window` tokens are
+    seen.  Returns out [n_q, Hq, d] of q's type; rows that no sequence has are not written (of a new
+    `out` they hold anything)."""
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("max_q: the most query tokens that cu_q gives a sequence")
+        max_q = 1
     tt = _t()
     dev = q.get_device()
     _same_device(dev, cache, block_tables, kv_lens, cu_q, out, workspace)
