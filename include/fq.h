@@ -408,8 +408,9 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  *   out[i, h] = sum_t softmax_t(scale * q[i, h] . k[t, g]) v[t, g],  g = h / (Hq / Hkv).
  *   q         n_q tokens of Hq heads of d coordinates, fp16 or bf16 (type); token and head strides
  *             in elements, coordinates contiguous.
- *   cu_q      [B + 1] int32: sequence b's query tokens are rows cu_q[b] .. cu_q[b + 1) of q (at most
- *             max_q of them).  NULL: one query token per sequence (n_q = B, max_q = 1).
+ *   cu_q      [B + 1] int32: sequence b's query tokens are rows cu_q[b] .. cu_q[b + 1) of q, at most
+ *             max_q of them: further ones are not computed.  A sequence whose counts fall or lie outside
+ *             0 .. n_q has none.  NULL: one query token per sequence (n_q = B, max_q = 1).
  *   kv_lens   [B] int32, clamped to 0 .. max_blocks * page: tokens of sequence b in the cache, its
  *             query tokens (its last ones) included.  Query token i of m sees the tokens below
  *             e = kv_len - m + i + 1 and, with window > 0, not below e - window.

@@ -34,10 +34,10 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   s.m = 1;
   if (a.cu_q) {
     s.q0 = __ldg(a.cu_q + b);
-    s.m = max(0, min(__ldg(a.cu_q + b + 1) - s.q0, a.max_q));
-    if (s.q0 < 0 || s.q0 > a.n_q - s.m) s.m = 0;
+    const int q1 = __ldg(a.cu_q + b + 1);
+    s.m = s.q0 >= 0 && q1 > s.q0 && q1 <= a.n_q ? q1 - s.q0 : 0;
   }
-  s.rows = s.m * r;
+  s.rows = min(s.m, a.max_q) * r;  // those past max_q keep their places and are left out
   s.blocks = (s.rows + NB - 1) / NB;
   s.cost = s.n;
   if (a.window > 0) s.cost = min(s.n, min(a.window, 1 << 30) + NB + kUnit);

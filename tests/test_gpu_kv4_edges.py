@@ -95,3 +95,28 @@ def test_many_small_weights_beside_a_large_one_are_not_lost(B, hq, hkv, dtype):
     rel = 2.0 ** -10 + 2 * n / 16 * 2.0 ** -24 + 2.0 ** -14 + (2 * (d + 8) * 2.0 ** -23 + (2.0 ** -10 if dtype == torch.bfloat16 and hq > 64 else 0)) * S
     half_eps = 2.0 ** -11 if dtype == torch.float16 else 2.0 ** -8
     assert (np.abs(got - want) <= (half_eps + rel) * want + lost + 2.0 ** -24).all(), (got[0, 0, :4], want[0, 0, :4])
+
+
+@pytest.mark.parametrize("hq", [4, 66])  # few rows of a kv head, and more than 64
+@pytest.mark.parametrize("cu", [[0, 2, 1, 9], [-3, 2, 4, 6], [0, 5, 7, 2 ** 31 - 1], [-2 ** 31, 2 ** 31 - 1, -2 ** 31, 8],
+                                [8, 8, 0, 2], [9, 10, 6, 8], [3, 8, 8, 8]])
+def test_counts_that_fall_or_lie_outside_the_queries(hq, cu):
+    """Such sequences have no rows, and of more than max_q query tokens the first are computed, each in its place."""
+    rng = np.random.default_rng(hq)
+    n_q, max_q, dtype = 8, 2, torch.float16
+    c = Cache(rng, [40, 33, 70], 1, 64, 32, 16)
+    q = _q(rng, n_q, hq, 64, dtype)
+    room = torch.full((n_q + 8, hq, 64), 7.0, dtype=dtype, device="cuda")
+    out = room[4:-4]
+    fq.fq_kv4_attn(q, _dev(c.host), _dev(c.tables), _dev(c.lens), 32, cu_q=_dev(np.array(cu, dtype=np.int64).astype(np.int32)),
+                   max_q=max_q, out=out)
+    assert (room[:4] == 7).all() and (room[-4:] == 7).all()
+    left = np.ones(n_q, dtype=bool)
+    for b in range(3):
+        lo, hi = cu[b], cu[b + 1]
+        if 0 <= lo < hi <= n_q:
+            rows = slice(lo, min(hi, lo + max_q))
+            want = ref.attend(_cpu(q[lo:hi].double()), c.host, c.tables[b:b + 1], c.lens[b:b + 1], 32, [0, hi - lo])
+            _check_attn(out[rows], *(w[:max_q] for w in want), 64, dtype, rows=max_q * hq)
+            left[rows] = False
+    assert (out[torch.from_numpy(left).cuda()] == 7).all()
