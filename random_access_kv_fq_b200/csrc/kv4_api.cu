@@ -1,5 +1,6 @@
 // extern "C" entry points of the 4-bit paged cache: argument validation and dispatch, as
 // fq_api.cu does for the codec (nothing is allocated, nothing synchronises, no state is kept).
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -102,8 +103,8 @@ fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
   if (need > 0 && (!workspace || workspace_bytes < need)) return FQ_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return FQ_ERR_ALIGNMENT;
   const AttnArgs a{q, type, n_q, Hq, d, q_token_stride, q_head_stride, cu_q, B, max_q, cache,
-                   n_blocks, Hkv, page, group, block_tables, max_blocks, kv_lens, window, scale,
-                   out, workspace};
+                   n_blocks, Hkv, page, group, block_tables, max_blocks, kv_lens,
+                   std::min(window, kMaxWindow), scale, out, workspace};
   return from_cuda(launch_attn(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -40,7 +40,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   s.rows = min(s.m, a.max_q) * r;  // those past max_q keep their places and are left out
   s.blocks = (s.rows + NB - 1) / NB;
   s.cost = s.n;
-  if (a.window > 0) s.cost = min(s.n, min(a.window, 1 << 30) + NB + kUnit);
+  if (a.window > 0) s.cost = min(s.n, a.window + NB + kUnit);
   s.cost = (s.cost + STEP - 1) / STEP + FIXED;
   return s;
 }

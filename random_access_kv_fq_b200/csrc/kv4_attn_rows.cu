@@ -133,7 +133,7 @@ struct Line {
   int fixed;
   __device__ __forceinline__ Line(const AttnArgs& a, const Seq& s, int r)
       : base(((int64_t)(s.n - s.m + 1) * r) >> 7),
-        top(a.window > 0 ? (((int64_t)min(a.window, 1 << 30) * r) >> 7) + 2 : (int64_t)1 << 40), fixed(kItemTiles * r) {}
+        top(a.window > 0 ? (((int64_t)a.window * r) >> 7) + 2 : (int64_t)1 << 40), fixed(kItemTiles * r) {}
   __device__ __forceinline__ int64_t cost(int block) const {
     return fixed + min(max(base + block + 1, (int64_t)0), top);
   }
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
       float m = -FLT_MAX, l = 0.f, kappa = 0.f;
       const uint32_t last_row = min(it.block * kRows + kRows, it.s.rows) - 1;
-      const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? hi - a.window : 0;
+      const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? max(0, hi - a.window) : 0;
       if (it.t0 < it.t1) {
         // this thread's half row of q, by a power of two in fp16, its keys' order of coordinates
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(it.s.q0 + tok) * a.q_tok + (int64_t)(it.head * r + hh) * a.q_head + half * (D / 2);

@@ -120,3 +120,17 @@ def test_counts_that_fall_or_lie_outside_the_queries(hq, cu):
             _check_attn(out[rows], *(w[:max_q] for w in want), 64, dtype, rows=max_q * hq)
             left[rows] = False
     assert (out[torch.from_numpy(left).cuda()] == 7).all()
+
+
+@pytest.mark.parametrize("hq", [4, 66])  # few rows of a kv head, and more than 64
+@pytest.mark.parametrize("window", [2 ** 30, 2 ** 31 - 9, 2 ** 31 - 1])
+def test_a_window_wider_than_any_sequence_is_none(hq, window):
+    """Sequences with more query tokens than tokens: their first rows end before the first token."""
+    rng = np.random.default_rng(window % 97)
+    qlens = [8, 1, 6, 12]
+    c = Cache(rng, [2, 70, 3, 300], 1, 64, 32, 16)
+    q, cu = _q(rng, sum(qlens), hq, 64, torch.bfloat16), np.concatenate([[0], np.cumsum(qlens)]).astype(np.int32)
+    out = fq.fq_kv4_attn(q, _dev(c.host), _dev(c.tables), _dev(c.lens), 32, cu_q=_dev(cu), max_q=12, window=window)
+    want = ref.attend(_cpu(q.double()), c.host, c.tables, c.lens, 32, cu, window)
+    _check_attn(out, *want, 64, torch.bfloat16, rows=12 * hq)
+    assert not out[:6].any() and (out[6:8] != 0).any()
