@@ -38,6 +38,14 @@ __host__ __device__ constexpr int value_word(int w, int t, int d) {
   return d == 128 ? w ^ (((t >> 1) & 1) << 3) : w;
 }
 
+// Waits until the copies of steps first .. last - 1 of a ring have landed: step t fills stage t % ring for the
+// (t / ring)th time.  wait(stage, parity) is a bounded wait for one phase.  A block whose waits gave up must
+// not end, nor write where the ring is, before that: a copy still on its way would land in whatever is there.
+template <typename Wait>
+__host__ __device__ inline void drain(uint32_t first, uint32_t last, uint32_t ring, Wait wait) {
+  for (uint32_t t = first; t < last; ++t) wait(t % ring, t / ring & 1);
+}
+
 struct WriteArgs {
   const void* k;
   const void* v;

@@ -96,6 +96,7 @@ struct Control {
   // scores may be computed: keys are there, and the weights in their place used up; are computed;
   // values and weights are there; are used up
   uint64_t s_ready[2], s_full[2], pv_ready[2], pv_done[2], q_full;
+  uint64_t products_done[2];  // all that the scores' and the weighted values' thread issued
   uint32_t tmem;
   int gave_up;
   int gone[2][8];  // units of the last eight tiles that are not there (bits), by each loader
@@ -105,8 +106,9 @@ struct Control {
 };
 static_assert(sizeof(Control) <= 1024, "in front of the operands");
 
-// A bounded wait that the whole block gives up together: from then on every wait returns at once, the
-// loader and the mma thread stop, and the other roles run to their end on whatever is there.
+// A bounded wait that the whole block gives up together: from then on every wait returns at once.  The
+// loaders and the threads that issue products stop, the other roles run to their end on whatever is there.  No
+// stage is filled again before its copies have landed, and copies and products in flight end before the block does.
 __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity) {
   for (uint32_t i = 0; i < ptx::kSpinLimit; ++i) {
     if (ptx::mbar_try(bar, parity & 1)) return true;
@@ -114,6 +116,12 @@ __device__ __forceinline__ bool wait(Control* c, uint64_t* bar, uint32_t parity)
   }
   *(volatile int*)&c->gave_up = 1;
   return false;
+}
+// Waits, with a limit, for all products that this thread has issued: they read shared memory and write tensor
+// memory that the block gives back at its end.  A barrier of its own, whose one phase nothing else completes.
+__device__ __forceinline__ void products_end(uint64_t* bar) {
+  ptx::umma_commit(bar);
+  ptx::mbar_wait(bar, 0);
 }
 // Warps that wait for an mbarrier are woken, and poll, whenever any mbarrier of the block moves: with all
 // of them doing so half of the issued instructions were polls.  So one softmax warp waits for the
@@ -333,6 +341,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       ptx::mbar_init(&ctl.pv_done[i], 1);
     }
     ptx::mbar_init(&ctl.q_full, kSoftmaxWarps);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(&ctl.products_done[i], 1);
     ptx::fence_mbar_init();
   }
   if (warp == 0) {
@@ -709,7 +718,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     if (warp == kSoftmaxWarps + kUnpackWarps) {
       // ---------------------------------------------------------------- scores
       constexpr uint32_t idesc = ptx::idesc_f16_f32(128, kTile);
-      bool ok = true;
+      bool ok = true, issued = false;
       uint32_t item = 0;
       for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
         const int tiles = it.t1 - it.t0;
@@ -730,16 +739,18 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                                  part > 0 || ks > 0 ? 1u : 0u);
             if (kExact) ptx::umma_f16_ts(d, tmem + C::QZ, ptx::sdesc_kmajor_noswz(base + 2 * C::kOp, 128, 256), idesc, 1u);
             ptx::umma_commit(&ctl.s_full[buf]);
+            issued = true;
           }
         }
         ok = __shfl_sync(~0u, (int)ok, 0);
         tile += tiles;
         ++item;
       }
+      if (issued) products_end(&ctl.products_done[0]);
     } else if (warp == kSoftmaxWarps + kUnpackWarps + 1) {
       // ---------------------------------------------------------------- weighted values
       constexpr uint32_t idesc = ptx::idesc_f16_f32(128, D) | (1u << 16);
-      bool ok = true;
+      bool ok = true, issued = false;
       for (bool begun = false; ok && it.next(a, r, begun); begun = true) {
         const int tiles = it.t1 - it.t0;
         if (lane == 0)
@@ -757,10 +768,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
                                  t > tile || part > 0 || ks > 0 ? 1u : 0u);
             ptx::umma_commit(&ctl.pv_done[buf]);
             ptx::umma_commit(&ctl.s_ready[buf]);
+            issued = true;
           }
         ok = __shfl_sync(~0u, (int)ok, 0);
         tile += max(tiles, 0);
       }
+      if (issued) products_end(&ctl.products_done[1]);
     } else {
       // ---------------------------------------------------------------- loaders
       const bool keys = warp == kSoftmaxWarps + kUnpackWarps + 2;
@@ -789,7 +802,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
             src = cache + ((((int64_t)id * a.hkv + head) << shift) + (u & ((1 << shift) - 1))) * C::UB;
           }
           const uint32_t slot = chunk % kRing;
-          if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[ring][slot], chunk / kRing - 1));
+          // a warp whose wait gave up has said that the stage is empty all the same: its copies may be on their way
+          if (chunk >= kRing) ok = __all_sync(~0u, wait(&ctl, &ctl.ring_empty[ring][slot], chunk / kRing - 1) && !*(volatile int*)&ctl.gave_up);
           if (!ok) break;
           if (lane / kChunkUnits == at / kChunkUnits) {
             uint64_t* bar = &ctl.ring_full[ring][slot];
@@ -810,23 +824,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
           __syncwarp();
         }
       }
-      // copies in flight land before the block ends, also where a wait gave up
-      if (!ok)
-        for (uint32_t t = chunk > kRing ? chunk - kRing : 0; t < chunk; ++t) ptx::mbar_wait(&ctl.ring_full[ring][t % kRing], (t / kRing) & 1);
+      // whoever's wait it was that gave up; where none did they have landed
+      drain(chunk > kRing ? chunk - kRing : 0, chunk, kRing, [&](uint32_t slot, uint32_t parity) { ptx::mbar_wait(&ctl.ring_full[ring][slot], parity); });
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (ctl.gave_up && warp == 0) {
-    // products that may be in flight: the last ones were committed to these
-    for (int i = 0; i < 2; ++i) {
-      for (uint32_t n = 0; n < 4096 && !ptx::mbar_try(&ctl.s_full[i], 0) && !ptx::mbar_try(&ctl.s_full[i], 1); ++n) {}
-      for (uint32_t n = 0; n < 4096 && !ptx::mbar_try(&ctl.pv_done[i], 0) && !ptx::mbar_try(&ctl.pv_done[i], 1); ++n) {}
-    }
-    if (lane == 0) atomicAdd(&g_kv4_rows_wait_timeouts, 1u);
-  }
+  if (ctl.gave_up && tid == 0) atomicAdd(&g_kv4_rows_wait_timeouts, 1u);
   if (warp == 0) ptx::tmem_dealloc(tmem, 512);
   asm volatile("griddepcontrol.launch_dependents;");
 }

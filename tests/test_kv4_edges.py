@@ -1,7 +1,11 @@
 """The 4-bit paged cache on the CPU: what the binding and the library refuse, or decide, on the host."""
+import os
+import subprocess
+
 import pytest
 
 import random_access_kv_fq_b200 as fq
+from random_access_kv_fq_b200 import build
 from tests import kv4_ref as ref
 
 torch = pytest.importorskip("torch")
@@ -21,3 +25,52 @@ def test_query_counts_need_their_maximum():
     for ok in (dict(cu_q=cu, max_q=2), dict(), dict(max_q=1)):  # as far as the tensors, which are not on a GPU
         with pytest.raises(ValueError, match="CUDA"):
             _call(**ok)
+
+
+DRAIN = r"""
+#include <cstdio>
+#include <initializer_list>
+#include <vector>
+#include "kv4.h"
+
+// An mbarrier as far as waits see it: a phase is over for a waiter if the current one's parity is not its own.
+struct Bar {
+  unsigned phases = 0, filled = 0;  // completed; times that the stage was filled
+  bool try_wait(unsigned parity) const { return (phases & 1) != parity; }
+};
+
+int main() {
+  // Probing both parities of a barrier says "done" of any barrier, and can wait for nothing.
+  for (unsigned phases : {0u, 1u, 2u, 3u}) {
+    Bar b;
+    b.phases = phases;
+    if (!b.try_wait(0) && !b.try_wait(1)) return 1;
+  }
+  // A ring of which the last copies, from any step on, are still in flight: each wait lets its own copy land.
+  for (unsigned ring : {2u, 4u, 8u})
+    for (unsigned issued = 0; issued <= 5 * ring; ++issued)
+      for (unsigned landed = issued > ring ? issued - ring : 0; landed <= issued; ++landed) {
+        std::vector<Bar> bars(ring);
+        for (unsigned t = 0; t < issued; ++t) {
+          ++bars[t % ring].filled;
+          if (t < landed) ++bars[t % ring].phases;
+        }
+        unsigned waits = 0;
+        fq::kv4::drain(issued > ring ? issued - ring : 0, issued, ring, [&](unsigned stage, unsigned parity) {
+          if (!bars[stage].try_wait(parity)) ++bars[stage].phases, ++waits;
+        });
+        for (const Bar& b : bars)
+          if (b.phases != b.filled) return 2;
+        if (waits != issued - landed) return 3;
+      }
+  return 0;
+}
+"""
+
+
+def test_every_copy_in_flight_is_waited_for(tmp_path):
+    src, exe = tmp_path / "drain.cpp", tmp_path / "drain"
+    src.write_text(DRAIN)
+    subprocess.run([build.nvcc(), "-std=c++17", "-I", build.CSRC, "-I", os.path.join(build.ROOT, "include"), "-o", str(exe), str(src)],
+                   check=True, timeout=300)
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0
