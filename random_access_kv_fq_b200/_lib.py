@@ -599,6 +599,8 @@ def fq_kv4_attn(q, cache, block_tables, kv_lens, group: int, cu_q=None, max_q: O
         raise ValueError("out: a contiguous tensor of q's shape and type")
     ws, ws_bytes = None, 0
     if workspace is not None:
+        if not workspace.is_contiguous():  # its elements would not be all that lies between its ends, nor need be there
+            raise ValueError("workspace: a contiguous tensor")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     else:
         ws_bytes = _kv4_size("fq_kv4_attn_workspace_bytes", B, hq, hkv, d, max_q, max_blocks, page)

@@ -134,3 +134,20 @@ def test_a_window_wider_than_any_sequence_is_none(hq, window):
     want = ref.attend(_cpu(q.double()), c.host, c.tables, c.lens, 32, cu, window)
     _check_attn(out, *want, 64, torch.bfloat16, rows=12 * hq)
     assert not out[:6].any() and (out[6:8] != 0).any()
+
+
+def test_a_workspace_has_to_have_the_bytes_that_it_counts():
+    rng = np.random.default_rng(3)
+    c = Cache(rng, [600, 20], 2, 64, 32, 16, max_blocks=400)
+    q, args = _q(rng, 2, 8, 64, torch.float16), (_dev(c.host), _dev(c.tables), _dev(c.lens), 32)
+    need = fq.fq_kv4_attn_workspace_bytes(2, 8, 2, 64, 1, 400, 16)
+    assert need > 0
+    ws = torch.empty(need + 64, dtype=torch.uint8, device="cuda")
+    for bad in (ws[:16].expand(need // 16 + 1, 16), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2]):
+        assert bad.numel() >= need
+        with pytest.raises(ValueError, match="contiguous"):
+            fq.fq_kv4_attn(q, *args, workspace=bad)
+    with pytest.raises(fq.FQError):
+        fq.fq_kv4_attn(q, *args, workspace=ws[:need - 1])
+    _check_attn(fq.fq_kv4_attn(q, *args, workspace=ws[:need].view(torch.float16)),
+                *ref.attend(_cpu(q.double()), c.host, c.tables, c.lens, 32), 64, torch.float16)
