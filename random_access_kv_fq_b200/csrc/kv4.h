@@ -38,6 +38,15 @@ __host__ __device__ constexpr int value_word(int w, int t, int d) {
   return d == 128 ? w ^ (((t >> 1) & 1) << 3) : w;
 }
 
+// place / cost, for a quotient below 2^30.  A 64-bit division takes a warp some hundred cycles at the start of
+// every call; this estimate is off by one at most below 2^22 items, and by 2^-22 of them above.
+__host__ __device__ inline int item_of(int64_t place, int cost) {
+  int item = (int)((float)place / (float)cost);
+  while ((int64_t)item * cost > place) --item;
+  while (place - (int64_t)item * cost >= cost) ++item;
+  return item;
+}
+
 // Waits until the copies of steps first .. last - 1 of a ring have landed: step t fills stage t % ring for the
 // (t / ring)th time.  wait(stage, parity) is a bounded wait for one phase.  A block whose waits gave up must
 // not end, nor write where the ring is, before that: a copy still on its way would land in whatever is there.

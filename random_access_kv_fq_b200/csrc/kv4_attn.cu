@@ -634,10 +634,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
         if (in_seq < cost) break;
         in_seq -= cost;
       }
-      // which of the sequence's items, all of one cost; the estimate is off by one at most
-      int item = (int)((float)in_seq / (float)s.cost);
-      if ((int64_t)item * s.cost > in_seq) --item;
-      if (in_seq - (int64_t)item * s.cost >= s.cost) ++item;
+      const int item = item_of(in_seq, s.cost);  // which of the sequence's items
       from = (int)(in_seq - (int64_t)item * s.cost);
       head = s.blocks == 1 ? item : item / s.blocks;
       block = item - head * s.blocks;

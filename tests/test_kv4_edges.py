@@ -68,9 +68,36 @@ int main() {
 """
 
 
-def test_every_copy_in_flight_is_waited_for(tmp_path):
-    src, exe = tmp_path / "drain.cpp", tmp_path / "drain"
-    src.write_text(DRAIN)
+def _run_cpp(tmp_path, source):
+    src, exe = tmp_path / "host.cpp", tmp_path / "host"
+    src.write_text(source)
     subprocess.run([build.nvcc(), "-std=c++17", "-I", build.CSRC, "-I", os.path.join(build.ROOT, "include"), "-o", str(exe), str(src)],
                    check=True, timeout=300)
-    assert subprocess.run([str(exe)], timeout=60).returncode == 0
+    return subprocess.run([str(exe)], timeout=60).returncode
+
+
+def test_every_copy_in_flight_is_waited_for(tmp_path):
+    assert _run_cpp(tmp_path, DRAIN) == 0
+
+
+ITEMS = r"""
+#include <random>
+#include "kv4.h"
+
+int main() {
+  std::mt19937_64 rng(1);
+  for (int i = 0; i < 2000000; ++i) {
+    const int cost = 4 + (int)(rng() % (1u << (rng() % 27)));
+    const int64_t items = 1 + (int64_t)(rng() % (1ull << (rng() % 31)));
+    // anywhere, and at an item's two ends
+    const int64_t n = (int64_t)(rng() % (uint64_t)items), at[] = {n * cost + (int64_t)(rng() % (uint64_t)cost), n * cost, n * cost + cost - 1};
+    for (int64_t place : at)
+      if (fq::kv4::item_of(place, cost) != n) return 1;
+  }
+  return 0;
+}
+"""
+
+
+def test_a_place_on_the_line_is_in_its_item(tmp_path):
+    assert _run_cpp(tmp_path, ITEMS) == 0
