@@ -74,7 +74,8 @@ fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, i
 size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int max_blocks,
                                    int page) {
   if ((d != 64 && d != 128) || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_q < 1 ||
-      max_blocks < 0 || !page_ok(page))
+      max_blocks < 0 || !page_ok(page) || B > kMaxRequests || (int64_t)max_blocks * page > (1 << 30) ||
+      max_q > (1 << 30) / Hq)
     return 0;
   return attn_workspace_bytes(B, Hq, Hkv, d, max_q, (int64_t)max_blocks * page);
 }

@@ -101,3 +101,10 @@ int main() {
 
 def test_a_place_on_the_line_is_in_its_item(tmp_path):
     assert _run_cpp(tmp_path, ITEMS) == 0
+
+
+def test_sizes_that_the_attention_refuses_need_no_workspace():
+    ws = fq.fq_kv4_attn_workspace_bytes
+    assert ws(8192, 32, 8, 128, 1, 1 << 20, 1024) > 0 and ws(8, 1024, 8, 128, 1 << 20, 64, 16) > 0
+    assert ws(8193, 32, 8, 128, 1, 64, 16) == 0 and ws(8, 32, 8, 128, 1, (1 << 20) + 1, 1024) == 0
+    assert ws(8, 1024, 8, 128, (1 << 20) + 1, 64, 16) == 0
