@@ -426,7 +426,7 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  * Precondition: the groups of tokens that are seen span less than 65504 (15 s and c s + z are fp16
  * numbers on the way).  A NaN in a key makes the rows that see it NaN; a NaN in a value those and,
  * as 0 times NaN, it may be other query tokens' rows of the sequence.
- * B <= 8192, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.
+ * B <= 8192, Hq <= 2^20, max_blocks * page <= 2^30, n_q * Hq <= 2^30, max_q * Hq <= 2^30.
  */
 fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
                       int64_t q_token_stride, int64_t q_head_stride, const int32_t* cu_q, int B,

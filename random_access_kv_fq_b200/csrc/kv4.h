@@ -19,6 +19,7 @@ namespace kv4 {
 constexpr int kUnit = 16;            // tokens of a unit
 constexpr int kMaxRequests = 8192;   // requests of one page step (their scans sit in shared memory)
 constexpr int kMinPage = 16, kMaxPage = 1024;
+constexpr int kMaxHeads = 1 << 20;  // query heads: what an item costs beside its tokens, kItemTiles of them, is an int
 constexpr int kMaxWindow = 1 << 30;  // the longest sequence: wider ones are cut to it, so that a place less a window is an int
 
 __host__ __device__ constexpr int unit_bytes(int d, int group) {

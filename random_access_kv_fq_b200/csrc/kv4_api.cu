@@ -74,8 +74,8 @@ fq_status fq_kv4_write(const void* k, const void* v, fq_dtype type, int64_t n, i
 size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int max_blocks,
                                    int page) {
   if ((d != 64 && d != 128) || B < 1 || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 || max_q < 1 ||
-      max_blocks < 0 || !page_ok(page) || B > kMaxRequests || (int64_t)max_blocks * page > (1 << 30) ||
-      max_q > (1 << 30) / Hq)
+      max_blocks < 0 || !page_ok(page) || B > kMaxRequests || Hq > kMaxHeads ||
+      (int64_t)max_blocks * page > (1 << 30) || max_q > (1 << 30) / Hq)
     return 0;
   return attn_workspace_bytes(B, Hq, Hkv, d, max_q, (int64_t)max_blocks * page);
 }
@@ -91,8 +91,8 @@ fq_status fq_kv4_attn(const void* q, fq_dtype type, int64_t n_q, int Hq, int d,
       max_q < 0 || window < 0 || (type != FQ_F16 && type != FQ_BF16) || !std::isfinite(scale))
     return FQ_ERR_INVALID_ARG;
   if (!cu_q && (n_q != B || max_q != 1)) return FQ_ERR_INVALID_ARG;
-  if (B > kMaxRequests || n_blocks > INT_MAX / page || (int64_t)max_blocks * page > (1 << 30) ||
-      n_q > (1 << 30) / Hq || max_q > (1 << 30) / Hq)
+  if (B > kMaxRequests || Hq > kMaxHeads || n_blocks > INT_MAX / page ||
+      (int64_t)max_blocks * page > (1 << 30) || n_q > (1 << 30) / Hq || max_q > (1 << 30) / Hq)
     return FQ_ERR_UNSUPPORTED;
   if (B == 0 || n_q == 0 || max_q == 0) return FQ_OK;
   if (!q || !out || !kv_lens || (n_blocks > 0 && !cache) || (max_blocks > 0 && !block_tables))

@@ -5,8 +5,9 @@ import subprocess
 import pytest
 
 import random_access_kv_fq_b200 as fq
-from random_access_kv_fq_b200 import build
+from random_access_kv_fq_b200 import _lib, build
 from tests import kv4_ref as ref
+from tests.test_kv4 import _attn_args
 
 torch = pytest.importorskip("torch")
 
@@ -108,3 +109,9 @@ def test_sizes_that_the_attention_refuses_need_no_workspace():
     assert ws(8192, 32, 8, 128, 1, 1 << 20, 1024) > 0 and ws(8, 1024, 8, 128, 1 << 20, 64, 16) > 0
     assert ws(8193, 32, 8, 128, 1, 64, 16) == 0 and ws(8, 32, 8, 128, 1, (1 << 20) + 1, 1024) == 0
     assert ws(8, 1024, 8, 128, (1 << 20) + 1, 64, 16) == 0
+
+
+def test_more_query_heads_than_an_items_cost_is_counted_for_are_refused():
+    for hq, status in ((1 << 20, 4), ((1 << 20) + 1, 2), (1 << 29, 2)):  # 4: taken, but for a missing workspace
+        assert _lib.lib().fq_kv4_attn(*_attn_args(n_q=1, B=1, hq=hq, hkv=1, ws=None)) == status
+        assert (fq.fq_kv4_attn_workspace_bytes(1, hq, 1, 64, 1, 4096, 16) > 0) == (status == 4)
