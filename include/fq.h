@@ -369,6 +369,9 @@ size_t fq_kv4_unit_bytes(int d, int group);
  *                    and pages left as they were, when it would pass max_blocks, when its tokens
  *                    pass n_slots, or when it needs pages and the pages needed up to and including
  *                    it are more than there are.
+ *                    Its tokens keep their place in cu_new: in the same step's attention, with lens_out
+ *                    for kv_lens, their rows are placed as if they were the last tokens held and mean
+ *                    nothing; the other requests' are right.
  * Precondition: the table entries of held pages and the free list hold distinct pages of the pool.
  * B <= 8192, max_blocks * page <= 2^30, n_slots <= 2^30.  One launch.
  */

@@ -486,7 +486,8 @@ def fq_page_step(lens, new_lens, block_tables, free_list, free_count, page: int,
     """One step of a paged cache's book-keeping (int32 CUDA tensors): requests of lens [B] tokens
     add new_lens [B] (negative: end) and grow block_tables [B, max_blocks] from the stack
     free_list[:free_count]; tables and free list are updated in place, free_count too unless
-    free_count_out is given.  Returns (lens_out [B], cu_new [B + 1], slots [n_slots], refused [1])."""
+    free_count_out is given.  Returns (lens_out [B], cu_new [B + 1], slots [n_slots], refused [1]);
+    the rows of refused requests in this step's attention mean nothing."""
     tt = _t()
     dev = lens.get_device()
     _same_device(dev, new_lens, block_tables, free_list, free_count, lens_out, free_count_out)

@@ -151,3 +151,29 @@ def test_a_workspace_has_to_have_the_bytes_that_it_counts():
         fq.fq_kv4_attn(q, *args, workspace=ws[:need - 1])
     _check_attn(fq.fq_kv4_attn(q, *args, workspace=ws[:need].view(torch.float16)),
                 *ref.attend(_cpu(q.double()), c.host, c.tables, c.lens, 32), 64, torch.float16)
+
+
+# ------------------------------------------------------------------ all three together
+
+@pytest.mark.parametrize("hq", [2, 6])
+def test_a_refused_request_leaves_the_others_of_its_step_alone(hq):
+    rng = np.random.default_rng(hq)
+    d, group, page, n_blocks, B = 64, 32, 16, 9, 4
+    dtype = torch.float16
+    pool = torch.full((n_blocks, 1, 1, ref.unit_bytes(d, group)), 0xFF, dtype=torch.uint8, device="cuda")
+    tables, free = torch.full((B, 3), -1, dtype=torch.int32, device="cuda"), _dev(rng.permutation(n_blocks).astype(np.int32))
+    lens, count = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.tensor([n_blocks], dtype=torch.int32, device="cuda")
+    for adds, turned_away in (([5, 20, 33, 1], []), ([2, 40, 9, 1], [1]), ([1, 3, 20, 14], [2])):
+        n = sum(adds)
+        new = _dev(np.array(adds, dtype=np.int32))
+        before = _cpu(lens)
+        lens, cu, slots, refused = fq.fq_page_step(lens, new, tables, free, count, page, n)
+        k, v, q = (_q(rng, n, h, d, dtype) for h in (1, 1, hq))
+        fq.fq_kv4_write(k, v, slots, pool, group)
+        out = fq.fq_kv4_attn(q, pool, tables, lens, group, cu_q=cu, max_q=max(adds))
+        assert int(refused) == len(turned_away)
+        assert _cpu(lens).tolist() == [int(a) + (0 if b in turned_away else m) for b, (a, m) in enumerate(zip(before, adds))]
+        want, A, S = ref.attend(_cpu(q.double()), _cpu(pool), _cpu(tables), _cpu(lens), group, _cpu(cu))
+        at = _cpu(cu)
+        rows = np.concatenate([np.arange(at[b], at[b + 1]) for b in range(B) if b not in turned_away])
+        _check_attn(out[torch.from_numpy(rows).cuda()], want[rows], A[rows], S[rows], d, dtype, rows=max(adds) * hq)
