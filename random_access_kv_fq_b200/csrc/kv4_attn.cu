@@ -702,40 +702,44 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       // a few units go through the code that checks each token: less code to fetch
       const bool clean = chunks > 2;
       const int all_end = past + tok0, all_first = a.window > 0 ? past + tok1 - a.window : 0;
-      for (int j = 0; j < chunks; ++j) {
+      // a wait that gives up ends the loop once the copies in flight had the time of another wait each to land
+      int landing = chunks;
+      for (int j = 0; j < landing; ++j) {
         if (((j * kChunk) & 31) == 0) gone = gone_next;
         const uint32_t at_stage = (count + j) % kStages, parity = (count + j) / kStages & 1;
         if (!__all_sync(~0u, ptx::mbar_try(&bars[warp][at_stage], parity)) &&
-            !__all_sync(~0u, ptx::mbar_wait(&bars[warp][at_stage], parity))) {
-          // this copy and those behind it have the time of another wait each to land
-          drain(count + j, count + min(chunks, j + kStages), kStages, [&](uint32_t stage, uint32_t p) { ptx::mbar_wait(&bars[warp][stage], p); });
+            !__all_sync(~0u, ptx::mbar_wait(&bars[warp][at_stage], parity)) && ok) {
           ok = false;
-          break;
+          landing = min(chunks, j + kStages);
+          --j;  // this one too
+          continue;
         }
-        const uint32_t skip = gone >> ((j * kChunk) & 31) & ((1u << kChunk) - 1);
-        const int pos0 = (base_u + u0 + j * kChunk) * kUnit;
-        typename W_::Place u = place;
-        const uint32_t off = at_stage * kChunk * UB;
-        u.k += off;
-        u.ks += off;
-        u.v += off;
-        u.vs += off;
-        if (clean && pos0 >= all_first && pos0 + kChunk * kUnit <= all_end && skip == 0) {
+        if (ok) {
+          const uint32_t skip = gone >> ((j * kChunk) & 31) & ((1u << kChunk) - 1);
+          const int pos0 = (base_u + u0 + j * kChunk) * kUnit;
+          typename W_::Place u = place;
+          const uint32_t off = at_stage * kChunk * UB;
+          u.k += off;
+          u.ks += off;
+          u.v += off;
+          u.vs += off;
+          if (clean && pos0 >= all_first && pos0 + kChunk * kUnit <= all_end && skip == 0) {
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i)
-            st.template unit<false>(typename W_::Place{u.k + i * UB, u.ks + i * UB, u.v + i * UB, u.vs + i * UB}, 0, 0, 0, lane);
-        } else {
+            for (int i = 0; i < kChunk; ++i)
+              st.template unit<false>(typename W_::Place{u.k + i * UB, u.ks + i * UB, u.v + i * UB, u.vs + i * UB}, 0, 0, 0, lane);
+          } else {
 #pragma unroll 1
-          for (int i = 0; i < kChunk; ++i) {
-            if (!((skip >> i) & 1)) st.template unit<true>(u, pos0 + i * kUnit, first, end, lane);
-            u.k += UB;
-            u.ks += UB;
-            u.v += UB;
-            u.vs += UB;
+            for (int i = 0; i < kChunk; ++i) {
+              if (!((skip >> i) & 1)) st.template unit<true>(u, pos0 + i * kUnit, first, end, lane);
+              u.k += UB;
+              u.ks += UB;
+              u.v += UB;
+              u.vs += UB;
+            }
           }
+          __syncwarp();
+          if (j + kStages < chunks) issue(j + kStages);
         }
-        __syncwarp();
-        if (j + kStages < chunks) issue(j + kStages);
       }
       count += chunks;
       st.finish_sums();
