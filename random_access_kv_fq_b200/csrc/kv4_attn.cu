@@ -13,8 +13,9 @@
 //            groups' sums of q (in two fp16 parts), so scores carry no 16-bit rounding: q itself
 //            is scaled to fp16 by a power of two per row.
 //   softmax  base 2, against a running maximum that moves only when a score passes it by 8 (kLow, kLag).
-//   values   O^T += V^T P^T with V = fp16(c s + z) and P in fp16, for fp16 outputs in two parts:
-//            one rounding of 2^-12 then, beside the output's own; bf16's own is 2^-9.
+//   values   O^T += V^T P^T with V = fp16(c s + z), which the product takes 16 bits of, off by at most
+//            2^-11.  P is fp16 too, for fp16 outputs in two parts, so that V's is the one rounding beside
+//            the output's own of 2^-11; beside bf16's of 2^-8 one part does.
 // A warp's unfinished ranges are joined in shared memory, a block's by the last block to leave a part
 // of the item.
 //
@@ -53,6 +54,19 @@ struct Part {
   float4 o[NT * D / 16 * 32];  // accumulators in fragment order
   float m[8 * NT], l[8 * NT];
 };
+
+// The cost of each of its row blocks: the units of the most tokens that one may see, and what is fixed.
+struct CostedSeq : Seq {
+  int cost;
+};
+template <int NB>
+__device__ __forceinline__ CostedSeq load_costed(const AttnArgs& a, int b, int r) {
+  CostedSeq s;
+  static_cast<Seq&>(s) = load_seq<NB>(a, b, r);
+  const int most = a.window > 0 ? min(s.n, a.window + NB + kUnit) : s.n;
+  s.cost = (most + kUnit - 1) / kUnit + kItemUnits;
+  return s;
+}
 
 // What a warp says of a part that it leaves.
 struct PartHeader {
@@ -107,7 +121,7 @@ struct Warp {
   static constexpr int NG = D / G, KB = D / 32, MT = D / 16, UB = kUnit * D + 128 * NG;
   static constexpr bool kTwoParts = __is_same(T, __half);
   uint32_t q[NT][KB][4];     // query fragments; odd ones over 16
-  uint32_t qz[NT][2];        // sums of q over the groups, two parts (the second word for NG = 8 only)
+  uint32_t qz[NT];           // sums of q over the groups, in two parts
   float kappa[NT][2];        // score scale of rows 2 t, 2 t + 1 of the tile
   int hi[NT][2], lo[NT][2];  // tokens that the rows see: [lo, hi)
   float o[NT][MT][4], m[NT][2], l[NT][2];  // m: kLow below the scores' maximum
@@ -214,7 +228,7 @@ struct Warp {
       } else {
         if (t < 2) w = u32(__halves2half2(none, part[t][0]));
       }
-      qz[nt][0] = w;
+      qz[nt] = w;
     }
     // the accumulators' columns are rows 2 t, 2 t + 1: their scale sits in lanes 8 t, 8 t + 4
 #pragma unroll
@@ -288,7 +302,7 @@ struct Warp {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       float acc[4];
-      mma8_first(acc, z0, z1, qz[nt][0]);
+      mma8_first(acc, z0, z1, qz[nt]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         x[nt][i] = fmaf(x[nt][i], 16777216.f, acc[i]);
@@ -575,13 +589,13 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
   // number `block` of the row blocks of (sequence b, kv head).
   int64_t left = 0, span = 1;
   int from = 0, b = 0, head = 0, block = 0;
-  Seq s = {};
+  CostedSeq s = {};
   if (own_blocks > 0) {
     // short contexts: a block to an item, shared out to its warps
     block = blockIdx.x % own_blocks;
     head = blockIdx.x / own_blocks % a.hkv;
     b = blockIdx.x / own_blocks / a.hkv;
-    s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
+    s = load_costed<NB>(a, b, r);
     if (block < s.blocks) {
       s.cost = kItemUnits + W;  // a W-th of the units each, whatever their number
       from = warp == 0 ? 0 : kItemUnits + warp;
@@ -594,7 +608,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
     int64_t* sums = reinterpret_cast<int64_t*>(smem);
     int64_t x = 0;
     for (int i = b0; i < b1; ++i) {
-      s = load_seq<NB, kUnit, kItemUnits>(a, i, r);
+      s = load_costed<NB>(a, i, r);
       x += (int64_t)(a.hkv * s.blocks) * s.cost;
     }
 #pragma unroll
@@ -629,7 +643,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       }
       int64_t in_seq = x0 - (lo > 0 ? sums[lo - 1] : 0);
       for (b = lo * per;; ++b) {
-        s = load_seq<NB, kUnit, kItemUnits>(a, b, r);
+        s = load_costed<NB>(a, b, r);
         const int64_t cost = (int64_t)(a.hkv * s.blocks) * s.cost;
         if (in_seq < cost) break;
         in_seq -= cost;
@@ -761,7 +775,7 @@ __global__ void __launch_bounds__(32 * kWarpsOf<NT, D>, 1) attn_kernel(AttnArgs 
       block = 0;
       if (++head == a.hkv) {
         head = 0;
-        do s = load_seq<NB, kUnit, kItemUnits>(a, ++b, r); while (s.blocks == 0);
+        do s = load_costed<NB>(a, ++b, r); while (s.blocks == 0);
       }
     }
   }

@@ -20,13 +20,11 @@ constexpr int kCtas = 148;  // one block per SM
 constexpr float kLow = 7.f, kLag = 8.f;
 
 struct Seq {
-  int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks
-  int cost;                    // of each of its row blocks: the most that one may see
+  int n, m, q0, rows, blocks;  // tokens, query tokens, first row of q, rows per kv head, row blocks of NB
+  int past;                    // tokens that the first query token sees, none if below 1
 };
 
-// Row blocks of NB rows; their cost is in steps of STEP tokens, FIXED of them for each row block's
-// queries and its end.
-template <int NB, int STEP, int FIXED>
+template <int NB>
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   Seq s;
   s.n = min(max(__ldg(a.kv_lens + b), 0), a.max_blocks * a.page);
@@ -39,9 +37,7 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int b, int r) {
   }
   s.rows = min(s.m, a.max_q) * r;  // those past max_q keep their places and are left out
   s.blocks = (s.rows + NB - 1) / NB;
-  s.cost = s.n;
-  if (a.window > 0) s.cost = min(s.n, a.window + NB + kUnit);
-  s.cost = (s.cost + STEP - 1) / STEP + FIXED;
+  s.past = s.n - s.m + 1;
   return s;
 }
 

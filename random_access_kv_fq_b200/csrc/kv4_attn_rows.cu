@@ -8,8 +8,8 @@
 //   products one thread issues S = Q K^T into one of two buffers of tensor memory, the next tile's under
 //            this tile's softmax, one issues O += P V with P in tensor memory;
 //   softmax  8 warps, two threads to a row: S out of tensor memory, weights P back into its place.
-// q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), half a step (2^-12) off.
-// For bf16 outputs, whose own rounding is 2^-9, keys and weights are fp16 numbers likewise.  For fp16
+// q is scaled to fp16 by a power of two per row.  Values are V = fp16(c s + z), at most half a step (2^-11) off.
+// For bf16 outputs, whose own rounding is 2^-8, keys and weights are fp16 numbers likewise.  For fp16
 // outputs neither may add to it:  s is split into its leading 7 bits and the rest, so that s_hi c and
 // s_lo c are fp16 numbers exactly, and
 //   S = Q (s_hi C)^T + Q (s_lo C)^T + qsum Z^T,
@@ -67,6 +67,8 @@ constexpr int kChunkUnits = 4;
 // registers a thread: 96 at launch, 20 warps x 96 >= 8 x 128 + 12 x 72; nothing is spilled
 constexpr int kSoftmaxRegs = 128, kOtherRegs = 72;
 
+constexpr int kItemBytes = 96;  // of a warp's Items
+
 template <int D>
 struct RowsPart {
   float4 o[D / 4][kRows];  // 32 rows' pieces lie together
@@ -86,7 +88,7 @@ struct Shape {
   static constexpr int kRing = D == 64 ? 8 : EXACT ? 2 : 4;  // what shared memory leaves
   static constexpr size_t kControl = 1024;
   static constexpr size_t kItems = kControl + 2 * kBuf + kRing * (kKeys + kValues);
-  static constexpr size_t kSmem = kItems + kWarps * 96;
+  static constexpr size_t kSmem = kItems + kWarps * kItemBytes;
   // tensor memory columns: [2] S, of which P takes the place (hi, then lo), O, Q and its sums
   static constexpr uint32_t S = 0, O = 256, Q = 384, QZ = 448;
 };
@@ -140,7 +142,7 @@ struct Line {
   int64_t base, top;
   int fixed;
   __device__ __forceinline__ Line(const AttnArgs& a, const Seq& s, int r)
-      : base(((int64_t)(s.n - s.m + 1) * r) >> 7),
+      : base(((int64_t)s.past * r) >> 7),
         top(a.window > 0 ? (((int64_t)a.window * r) >> 7) + 2 : (int64_t)1 << 40), fixed(kItemTiles * r) {}
   __device__ __forceinline__ int64_t cost(int block) const {
     return fixed + min(max(base + block + 1, (int64_t)0), top);
@@ -159,12 +161,12 @@ struct Line {
 // The items of a block's range of the line, one at a time, the same in every role.  Each warp has its own
 // in shared memory: in registers they would be spilled.
 template <int D>
-struct Items {
+struct alignas(16) Items {
   int64_t left, from;
   int b, head, block;  // block: its row block
   Seq s;
   // of the current item
-  int end, first, base_u, t0, t1, past;
+  int end, first, base_u, t0, t1;
   int64_t to, cost;
   __device__ __forceinline__ bool next(const AttnArgs& a, int r, bool begun) {
     __syncwarp();
@@ -177,7 +179,7 @@ struct Items {
           x.block = 0;
           if (++x.head == a.hkv) {
             x.head = 0;
-            do x.s = load_seq<kRows, kTile, kItemTiles>(a, ++x.b, r); while (x.s.blocks == 0);
+            do x.s = load_seq<kRows>(a, ++x.b, r); while (x.s.blocks == 0);
           }
         }
       }
@@ -187,10 +189,9 @@ struct Items {
       x.cost = line.cost(x.block);
       x.to = min(x.cost, x.from + x.left);
       x.left -= x.to - x.from;
-      x.past = s.n - s.m + 1;
       const uint32_t row0 = x.block * kRows, row1 = min(x.block * kRows + kRows, s.rows) - 1;
-      x.end = max(0, x.past + (int)(row1 / (uint32_t)r));
-      x.first = a.window > 0 ? max(0, x.past + (int)(row0 / (uint32_t)r) - a.window) : 0;
+      x.end = max(0, s.past + (int)(row1 / (uint32_t)r));
+      x.first = a.window > 0 ? max(0, s.past + (int)(row0 / (uint32_t)r) - a.window) : 0;
       x.base_u = x.first / kUnit;
       const int tiles = x.end > x.first ? (x.end - x.base_u * kUnit + kTile - 1) / kTile : 0;
       const int64_t full = x.cost - line.fixed;
@@ -356,14 +357,14 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
 
   // The line of all items' costs, cut into one range per block; the thread whose sequences hold the
   // range's start tells the block.
-  static_assert(sizeof(Items<D>) == 96, "");
+  static_assert(sizeof(Items<D>) == kItemBytes, "");
   Items<D>& it = reinterpret_cast<Items<D>*>(raw_smem + C::kItems)[warp];
   {
     Items<D> x = {};
     const int per = (a.B + 32 * kWarps - 1) / (32 * kWarps), b0 = tid * per, b1 = min(a.B, b0 + per);
     int64_t mine = 0;
     for (int i = b0; i < b1; ++i) {
-      x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+      x.s = load_seq<kRows>(a, i, r);
       mine += a.hkv * Line(a, x.s, r).sum(x.s.blocks);
     }
     int64_t sum = mine;
@@ -384,7 +385,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     const int64_t x0 = blockIdx.x * span;
     for (int i = b0; i < b1 && below <= x0; ++i) {
       if (per > 1) {
-        x.s = load_seq<kRows, kTile, kItemTiles>(a, i, r);
+        x.s = load_seq<kRows>(a, i, r);
         mine = a.hkv * Line(a, x.s, r).sum(x.s.blocks);
       }
       if (x0 < below + mine) {
@@ -400,7 +401,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
     x.from = x.b = x.head = x.block = 0;
     if (x.left > 0) {
       x.b = ctl.start_b;
-      x.s = load_seq<kRows, kTile, kItemTiles>(a, x.b, r);
+      x.s = load_seq<kRows>(a, x.b, r);
       const Line line(a, x.s, r);
       const int64_t head = line.sum(x.s.blocks);
       x.head = (int)(ctl.start_in / head);
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) rows_kernel(AttnArgs a, int pa
       const uint32_t tok = in ? row / r : 0, hh = in ? row - tok * r : 0;
       float m = -FLT_MAX, l = 0.f, kappa = 0.f;
       const uint32_t last_row = min(it.block * kRows + kRows, it.s.rows) - 1;
-      const int hi = it.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? max(0, hi - a.window) : 0;
+      const int hi = it.s.past + (int)(min(row, last_row) / (uint32_t)r), lo = a.window > 0 ? max(0, hi - a.window) : 0;
       if (it.t0 < it.t1) {
         // this thread's half row of q, by a power of two in fp16, its keys' order of coordinates
         const uint16_t* src = static_cast<const uint16_t*>(a.q) + (int64_t)(it.s.q0 + tok) * a.q_tok + (int64_t)(it.head * r + hh) * a.q_head + half * (D / 2);
