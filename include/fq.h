@@ -422,10 +422,12 @@ size_t fq_kv4_attn_workspace_bytes(int B, int Hq, int Hkv, int d, int max_q, int
  *             anything.
  *   out       [n_q, Hq, d] of `type`, 16-byte aligned.  A row that sees no token is 0; rows that no
  *             sequence has are left as they were.  A token whose weight is below 2^-32
- *             of the row's largest may count as 0.
+ *             of the row's largest may count as 0.  No other array may overlap it.
  *   workspace fq_kv4_attn_workspace_bytes(...) bytes, 16-byte aligned (NULL where that is 0), owned by the
  *             caller, of any content, and overwritten; calls that may overlap (two streams, two captured
  *             graphs) need one each.
+ * The kernel is chosen by max_q * Hq / Hkv: sequences of one or a few query tokens are faster in a call
+ * of their own than beside long chunks.
  * Precondition: the groups of tokens that are seen span less than 65504 (15 s and c s + z are fp16
  * numbers on the way).  A NaN in a key makes the rows that see it NaN; a NaN in a value those and,
  * as 0 times NaN, it may be other query tokens' rows of the sequence.

@@ -117,9 +117,9 @@ size_t attn_rows_workspace_bytes(int d);
 cudaError_t wait_timeouts_kv4(bool clear, unsigned* count);  // as those in fq_internal.h
 cudaError_t wait_timeouts_kv4_rows(bool clear, unsigned* count);
 
-// Rows of a kv head up to which the register-fed kernel is the faster one (24 sequences of 6,000 tokens, 4
-// kv heads, 1 to n drafted tokens, d = 128: 32 rows 49 us against 74, 48 rows 61 against 74, 64 rows 75
-// against 74; d = 64: 33 against 66, 38 against 66, 47 against 66).
+// Rows of a kv head, by a call's max_q, up to which the register-fed kernel runs: where the two meet for d = 128
+// (24 sequences of 6,000 tokens, 4 kv heads, 1 to n drafted tokens: 32 rows 49 us against 75, 48 rows 61, 64
+// rows 75).  For d = 64 they would meet later: 33 us against 68, 39, and 48 at 64 rows.
 constexpr int64_t kFewRows = 64;
 
 }  // namespace kv4

@@ -22,11 +22,13 @@
 // mma.sync and not tcgen05: the products of decode are 8 to 16 rows wide, operands come out of
 // registers, and the tensor pipe has three quarters of its time left at the HBM bound.
 //
-// Measured: 64 sequences of 1 to 8,191 tokens, 32 query and 8 kv heads of 128, bf16, 342 MB: 71 us, 4,790
-// GB/s, 0.73 of a copy's; issue slots 63 % busy, of the rest ~10,000 cycles are the way to the first unit
-// and ~12,000 the joins.  16 sequences of 32K tokens, 4 kv heads of 64, fp16, 168 MB: 49 us, 3,420 GB/s;
-// bound by issue (235 warp instructions a unit of 1,280 bytes).  24 sequences of up to 12K tokens behind a
-// window of 4,096, up to 42 rows a kv head: 41 us; each 16 rows unpack the units again.
+// Measured: 64 sequences of 1 to 8,191 tokens, 32 query and 8 kv heads of 128, bf16, 342 MB: 71 us, 4,800
+// GB/s, 0.73 of a copy's; issue slots 61 % busy, of the rest ~10,000 cycles are the way to the first unit
+// and ~12,000 the joins.  16 sequences of 32K tokens, 4 kv heads of 64, fp16, 168 MB: 49 us, 3,420 GB/s, 0.52;
+// neither memory (39 % busy) nor issue (62 %, 231 warp instructions a unit of 1,280 bytes) binds it but the
+// results that a warp waits for: of 7.5 cycles an instruction 1.7 are a fixed latency, 0.8 the matrix pipe, 0.5
+// barriers.  24 sequences of up to 12K tokens behind a window of 4,096, up to 42 rows a kv head: 41 us; each 16
+// rows unpack the units again.
 #include <atomic>
 #include <cfloat>
 

@@ -18,11 +18,11 @@
 // score passes it by 8 (kLow, kLag); moving it rescales O in tensor memory.
 //
 // A product of 128 x 128 x 16 takes 64 cycles (of 128 x 64 x 16: 50 to 57, so tiles are 128 tokens), so
-// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  It takes about 3,700
-// and 4,000 (3 chunks of up to 1,024 queries over up to 8K tokens, 32 query and 8 kv heads: 218 and 247 us,
-// 600 and 530 TFLOP/s): 9,000 warp instructions of unpacking and softmax a tile (fp16), and roles whose code
-// together does not stay in the instruction caches (a seventh of the stalls).  A change of item takes 10,000
-// to 15,000 cycles, so ranges are cut by tokens and parts of one tile are not made.
+// a tile of d = 128 needs 1,024 cycles of the tensor pipe for bf16 and 2,112 for fp16.  Of a call's time a tile
+// takes about 3,300 and 3,800 (3 chunks of up to 1,024 queries over up to 8K tokens, 32 query and 8 kv heads: 206
+// to 220 us, from run to run, and 249; 600 to 640 and 530 TFLOP/s): 9,200 warp instructions of unpacking and
+// softmax a tile (fp16), which keep the issue slots 68 % and the tensor pipe 50 % busy.  A change of item takes
+// 10,000 to 15,000 cycles, so ranges are cut by tokens and parts of one tile are not made.
 // Measured and not kept: 8 unpacking warps more, 16 softmax warps, softmax groups on
 // alternate tiles, asynchronous copies by the unpacking warps.
 #include <atomic>

@@ -10,7 +10,8 @@
 // order (1) all reads of lens and free_count before they may be overwritten in place and (2)
 // released pages before they are handed out again.  A warp writes 32 or 256 slots at a time: it finds
 // the requests of the first and the last by bisection and its lanes search only between them.
-// Measured: 256 decodes 5.0 us; 2,048 requests with prompts, releases and 262,144 slots 15 us.
+// Measured: 256 decodes 5.0 to 5.4 us; 2,048 requests with prompts, releases and 262,144 slots 15 us, on 16
+// multiprocessors and with a second barrier of the cluster between released pages and new ones.
 #include <atomic>
 #include <climits>
 
